@@ -8,3 +8,5 @@ binding.  Build with ``python -m bit_quantized_shampoo_amd.build``.
 from ._lib import LIB_PATH, Shampoo4Error  # noqa: F401
 from .shampoo4 import (Shampoo4Blocks, Shampoo4Config, codebook, dequantize,  # noqa: F401
                        gemm_batched, inverse_root, plan, quantize)
+from .train import (Act8, act8_load, act8_store, act8_weight_grad, activation_backward,  # noqa: F401
+                    activation_forward, embedding, embedding_grad, policy_loss, token_logprobs)

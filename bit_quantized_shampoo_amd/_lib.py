@@ -41,6 +41,17 @@ EXPORTED = [
     "shampoo4_gemm_batched_static", "shampoo4_gemm_batched_ex",
 ]
 
+# the training operators (include/shampoo4_train.h)
+EXPORTED_TRAIN = [
+    "shampoo4_act8_bytes", "shampoo4_act8_store", "shampoo4_act8_load", "shampoo4_activation_forward",
+    "shampoo4_activation_backward", "shampoo4_act8_weight_grad_workspace_bytes", "shampoo4_act8_weight_grad",
+    "shampoo4_embedding", "shampoo4_embedding_grad_workspace_bytes", "shampoo4_embedding_grad",
+    "shampoo4_policy_loss_workspace_bytes", "shampoo4_policy_loss", "shampoo4_token_logprobs",
+]
+F32, BF16, F16 = 0, 1, 2
+ACT_SILU, ACT_GELU = 0, 1
+ACT8_ROWS, ACT8_PITCH = 32, 16
+
 GRAFT_SGD, GRAFT_ADAM = 0, 1
 GEMM_AUTO, GEMM_FP32, GEMM_X3 = 0, 1, 2
 GEMM_STATIC_MAX = 2048
@@ -70,6 +81,11 @@ class GraftConfig(ctypes.Structure):
 class GraftIo(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("ldw", ctypes.c_int64), ("M", ctypes.c_void_p),
                 ("V", ctypes.c_void_p)]
+
+
+class PolicyConfig(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("grad_scale", ctypes.c_float)]
 
 
 class Shampoo4Error(RuntimeError):
@@ -138,6 +154,21 @@ def lib() -> ctypes.CDLL:
         "shampoo4_timing_report": (st, [vp, ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_char_p),
                                         ctypes.POINTER(i64), ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+        "shampoo4_act8_bytes": (st, [i64, i64, ctypes.POINTER(sz), ctypes.POINTER(sz)]),
+        "shampoo4_act8_store": (st, [i32, i64, i64, vp, i64, vp, vp, vp]),
+        "shampoo4_act8_load": (st, [i32, i64, i64, vp, vp, vp, i64, vp]),
+        "shampoo4_activation_forward": (st, [i32, i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp,
+                                             vp]),
+        "shampoo4_activation_backward": (st, [i32, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp]),
+        "shampoo4_act8_weight_grad_workspace_bytes": (sz, [i64, i64, i64]),
+        "shampoo4_act8_weight_grad": (st, [i32, i64, i64, i64, f32, vp, i64, vp, vp, f32, vp, i64, vp, sz, vp]),
+        "shampoo4_embedding": (st, [i32, i32, i64, i64, i64, vp, i64, vp, f32, vp, i64, vp]),
+        "shampoo4_embedding_grad_workspace_bytes": (sz, [i64, i64, i64]),
+        "shampoo4_embedding_grad": (st, [i32, i32, i64, i64, i64, vp, i64, vp, f32, i32, vp, i64, vp, sz, vp]),
+        "shampoo4_policy_loss_workspace_bytes": (sz, [i32, i64, i64]),
+        "shampoo4_policy_loss": (st, [ctypes.POINTER(PolicyConfig), i32, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp,
+                                      vp, vp, vp, i64, vp, sz, vp]),
+        "shampoo4_token_logprobs": (st, [i32, i32, i64, i64, vp, i64, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

@@ -1,0 +1,534 @@
+// Embedding lookup and its gradient by sorted tokens.
+//
+// Lookup: a stream of rows, eight elements a thread.
+//
+// Gradient: G[v] = scale * sum of dout[t] over the tokens t with id v.
+//  1. The positions are sorted by id, stably: least significant digit first, digits of up to
+//     9 bits (two passes up to 262143 words).  A wave ranks 64 ids at a time: nine ballots
+//     give each lane the lanes that share its digit, its rank among them and their number.
+//     Up to SMALL_T tokens one workgroup sorts in LDS, in one launch; beyond, a pass is two
+//     launches over blocks of SORT_TILE tokens (digit counts, then ranks and scatter).
+//     Without accumulation the other workgroups of these launches write G's zeros: the fill
+//     is bound by HBM and the sort by latency, so the sort costs next to nothing beside it.
+//  2. Sums over chunks of CHUNK sorted positions, one wave for 512 columns of a chunk: a run
+//     of equal ids inside a chunk is stored as a row of G; a run that crosses the chunk's
+//     ends goes to a partial row.  Every load address is known before the first sum, so
+//     eight rows are in flight.
+//  3. Runs over several chunks: one workgroup per run and 512 columns adds the partial rows,
+//     eight waves each every eighth, joined in a fixed order.
+// The order of every sum follows from the ids alone: no floating atomics.
+#include <algorithm>
+
+#include "train_common.hpp"
+#include "train.hpp"
+
+namespace s4 {
+
+namespace {
+
+constexpr int RADIX_BITS = 9;                // most bits of a digit
+constexpr int BINS = 1 << RADIX_BITS;
+constexpr int SMALL_T = 16384;               // one workgroup: 16 waves of up to 16 rounds
+constexpr int SMALL_WAVES = 16;
+constexpr int TILE_WAVES = 8;
+constexpr int TILE_ROUNDS = 8;
+constexpr int SORT_TILE = TILE_WAVES * TILE_ROUNDS * 64;
+constexpr int CHUNK = 16;                    // sorted positions per wave
+constexpr int COLS = 512;                    // columns per wave
+constexpr int JOIN_WAVES = 8;
+
+int bit_length(uint64_t v) {
+    int n = 0;
+    while (v) { ++n; v >>= 1; }
+    return n;
+}
+
+__device__ __forceinline__ int64_t id_at(const void* ids, int id64, int64_t i) {
+    return id64 ? ldg((const int64_t*)ids + i) : (int64_t)ldg((const int32_t*)ids + i);
+}
+// Sort key of a token: its id, or `vocab` (behind every row) for one that has none.
+__device__ __forceinline__ uint32_t key_at(const void* ids, int id64, int64_t vocab, int64_t i) {
+    const int64_t id = id_at(ids, id64, i);
+    return (uint32_t)(id >= 0 && id < vocab ? id : vocab);
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void embedding_kernel(Embed e, uint32_t nvec, uint64_t total) {
+    for (uint64_t i = blockIdx.x * 256ull + threadIdx.x; i < total; i += gridDim.x * 256ull) {
+        const uint64_t t = i / nvec;
+        const int64_t c = (int64_t)(i - t * nvec) * 8;
+        const int64_t id = id_at(e.ids, e.id64, (int64_t)t);
+        const int n = (int)min((int64_t)8, e.dim - c);
+        typename Vec8<T>::Raw r = {};
+        if (id >= 0 && id < e.vocab) {
+            r = load8_n((const T*)e.table + id * e.ldtable + c, n);
+            r = Vec8<T>::put(Vec8<T>::get(r) * e.scale);
+        }
+        store8_n((T*)e.out + (int64_t)t * e.ldout + c, r, n);
+    }
+}
+
+// Part `part` of `parts` of the zeros of G, by workgroups 0 .. nblk - 1 of this launch.
+struct Fill {
+    float* g;                 // NULL: nothing to fill
+    int64_t rows, cols, ld;
+    int part, parts;
+};
+__device__ void fill_zeros(const Fill& f, int64_t blk, int64_t nblk) {
+    // contiguous rows are one row
+    const bool flat = f.ld == f.cols;
+    const int64_t cols = flat ? f.rows * f.cols : f.cols;
+    const int64_t rows = flat ? 1 : f.rows;
+    const int64_t per = (int64_t)blockDim.x * 4;
+    const int64_t chunks = (cols + per - 1) / per;           // pieces of a row
+    const int64_t n = rows * chunks;
+    const int64_t b0 = n * f.part / f.parts, b1 = n * (f.part + 1) / f.parts;
+    for (int64_t i = b0 + blk; i < b1; i += nblk) {
+        const int64_t r = i / chunks;
+        const int64_t c = (i - r * chunks) * per + threadIdx.x * 4;
+        float* p = f.g + r * f.ld + c;
+        if (c + 4 <= cols) {
+            typedef floatx4 M __attribute__((aligned(4)));
+            using G = __attribute__((address_space(1))) M;
+            *(G*)p = floatx4{0.f, 0.f, 0.f, 0.f};
+        } else {
+            for (int64_t j = c; j < cols; ++j) stg(f.g + r * f.ld + j, 0.f);
+        }
+    }
+}
+
+// Lanes of this wave with the same digit as this one (live lanes only).
+__device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool live, int bits) {
+    uint64_t m = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (digit >> b) & 1;
+        const uint64_t w = __ballot(one && live);
+        m &= one ? w : ~w;
+    }
+    return m;
+}
+
+// Stable ranks of a workgroup's items by digit.  Wave w's item of round r is number
+// (w rounds + r) 64 + lane.  cnt [waves][bins] counts each wave's digits; on return rank[r]
+// is the item's rank among its wave's items of the same digit.
+template <int ROUNDS>
+__device__ __forceinline__ void wave_ranks(const uint32_t (&digit)[ROUNDS], const bool (&live)[ROUNDS], int bits,
+                                           uint32_t* cnt, uint32_t (&rank)[ROUNDS], int rounds) {
+    const int lane = threadIdx.x & 63;
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+        if (r < rounds) {
+            const uint64_t m = same_digit(digit[r], live[r], bits);
+            uint32_t old = 0;
+            if (live[r]) old = cnt[digit[r]];
+            rank[r] = old + __popcll(m & below);
+            // the next round reads what this one's first lane writes: LDS accesses of a wave
+            // execute in order, and the fences keep the compiler to it
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (live[r] && (m & below) == 0) cnt[digit[r]] = old + __popcll(m);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        }
+    }
+}
+
+// Turns cnt [waves][bins] into each wave's first place per digit, and returns through
+// `tot` (LDS, bins) each digit's first place in the workgroup's own order.
+__device__ __forceinline__ void digit_places(uint32_t* cnt, int waves, int bins, uint32_t* tot, uint32_t* wsum) {
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    uint32_t s = 0;
+    if (tid < bins)
+        for (int w = 0; w < waves; ++w) {
+            const uint32_t c = cnt[w * BINS + tid];
+            cnt[w * BINS + tid] = s;
+            s += c;
+        }
+    uint32_t inc = s;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = (uint32_t)__shfl_up((int)inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 63) wsum[wv] = inc;
+    __syncthreads();
+    uint32_t before = 0;
+    for (int w = 0; w < wv; ++w) before += wsum[w];
+    if (tid < bins) tot[tid] = before + inc - s;
+    __syncthreads();
+}
+
+// Up to SMALL_T tokens: workgroup 0 sorts (id, position) packed in one word (`pos_bits` low
+// bits of position) in LDS; the others fill zeros.
+__global__ __launch_bounds__(1024) void sort_small_kernel(const void* ids, int id64, int64_t vocab, int tokens,
+                                                          int passes, int bits, int pos_bits, uint32_t* skey,
+                                                          uint32_t* spos, Fill fill) {
+    __shared__ uint32_t buf[SMALL_T];
+    __shared__ uint32_t cnt[SMALL_WAVES * BINS];
+    __shared__ uint32_t tot[BINS];
+    __shared__ uint32_t wsum[SMALL_WAVES];
+    if (blockIdx.x > 0) {
+        fill_zeros(fill, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int rounds = (tokens + 1023) / 1024;
+    const int bins = 1 << bits;
+    uint32_t item[16], digit[16], rank[16];
+    bool live[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int i = (wv * rounds + r) * 64 + lane;
+        live[r] = r < rounds && i < tokens;
+        item[r] = live[r] ? key_at(ids, id64, vocab, i) << pos_bits | (uint32_t)i : 0u;
+    }
+    for (int p = 0; p < passes; ++p) {
+        for (int i = tid; i < SMALL_WAVES * BINS; i += 1024) cnt[i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            if (p > 0 && live[r]) item[r] = buf[(wv * rounds + r) * 64 + lane];
+            digit[r] = (item[r] >> (pos_bits + p * bits)) & (uint32_t)(bins - 1);
+        }
+        wave_ranks<16>(digit, live, bits, cnt + wv * BINS, rank, rounds);
+        __syncthreads();
+        digit_places(cnt, SMALL_WAVES, bins, tot, wsum);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            if (live[r]) buf[tot[digit[r]] + cnt[wv * BINS + digit[r]] + rank[r]] = item[r];
+        __syncthreads();
+    }
+    for (int i = tid; i < tokens; i += 1024) {
+        stg(skey + i, buf[i] >> pos_bits);
+        stg(spos + i, buf[i] & ((1u << pos_bits) - 1));
+    }
+}
+
+struct SortPass {
+    const void* ids;          // pass 0: the ids; else NULL
+    const uint32_t* key;
+    const uint32_t* pos;
+    uint32_t* key_out;
+    uint32_t* pos_out;
+    uint32_t* hist;           // [blocks][bins]
+    int64_t vocab, tokens;
+    int id64, shift, bits, nblk;
+};
+
+__global__ __launch_bounds__(512) void sort_count_kernel(SortPass s, Fill fill) {
+    __shared__ uint32_t h[BINS];
+    if ((int)blockIdx.x >= s.nblk) {
+        fill_zeros(fill, blockIdx.x - s.nblk, gridDim.x - s.nblk);
+        return;
+    }
+    const int tid = threadIdx.x, bins = 1 << s.bits;
+    h[tid] = 0;
+    __syncthreads();
+    const int64_t i0 = (int64_t)blockIdx.x * SORT_TILE;
+#pragma unroll
+    for (int r = 0; r < SORT_TILE / 512; ++r) {
+        const int64_t i = i0 + r * 512 + tid;
+        if (i < s.tokens) {
+            const uint32_t k = s.ids ? key_at(s.ids, s.id64, s.vocab, i) : ldg(s.key + i);
+            atomicAdd(&h[(k >> s.shift) & (uint32_t)(bins - 1)], 1u);
+        }
+    }
+    __syncthreads();
+    if (tid < bins) stg(s.hist + (int64_t)blockIdx.x * bins + tid, h[tid]);
+}
+
+__global__ __launch_bounds__(512) void sort_scatter_kernel(SortPass s, Fill fill) {
+    __shared__ uint32_t cnt[TILE_WAVES * BINS];
+    __shared__ uint32_t wsum[TILE_WAVES];
+    if ((int)blockIdx.x >= s.nblk) {
+        fill_zeros(fill, blockIdx.x - s.nblk, gridDim.x - s.nblk);
+        return;
+    }
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, bins = 1 << s.bits;
+    for (int i = tid; i < TILE_WAVES * BINS; i += 512) cnt[i] = 0;
+    __syncthreads();
+    uint32_t key[TILE_ROUNDS], digit[TILE_ROUNDS], rank[TILE_ROUNDS];
+    bool live[TILE_ROUNDS];
+    const int64_t i0 = (int64_t)blockIdx.x * SORT_TILE + wv * TILE_ROUNDS * 64 + lane;
+#pragma unroll
+    for (int r = 0; r < TILE_ROUNDS; ++r) {
+        const int64_t i = i0 + r * 64;
+        live[r] = i < s.tokens;
+        key[r] = 0;
+        if (live[r]) key[r] = s.ids ? key_at(s.ids, s.id64, s.vocab, i) : ldg(s.key + i);
+        digit[r] = (key[r] >> s.shift) & (uint32_t)(bins - 1);
+    }
+    wave_ranks<TILE_ROUNDS>(digit, live, s.bits, cnt + wv * BINS, rank, TILE_ROUNDS);
+    __syncthreads();
+    // places: all tokens of smaller digits, then this digit's in earlier blocks
+    uint32_t all = 0, before = 0;
+    if (tid < bins)
+        for (int b = 0; b < s.nblk; ++b) {
+            const uint32_t c = ldg(s.hist + (int64_t)b * bins + tid);
+            all += c;
+            before += b < (int)blockIdx.x ? c : 0u;
+        }
+    uint32_t inc = all;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t y = (uint32_t)__shfl_up((int)inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 63) wsum[wv] = inc;
+    __syncthreads();
+    uint32_t prior = 0;
+    for (int w = 0; w < wv; ++w) prior += wsum[w];
+    if (tid < bins) {
+        uint32_t at = prior + inc - all + before;
+        for (int w = 0; w < TILE_WAVES; ++w) {
+            const uint32_t c = cnt[w * BINS + tid];
+            cnt[w * BINS + tid] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < TILE_ROUNDS; ++r)
+        if (live[r]) {
+            const int64_t i = i0 + r * 64;
+            const uint32_t at = cnt[wv * BINS + digit[r]] + rank[r];
+            stg(s.key_out + at, key[r]);
+            stg(s.pos_out + at, s.ids ? (uint32_t)i : ldg(s.pos + i));
+        }
+}
+
+struct RunSum {
+    const void* dout;
+    const uint32_t* key;      // sorted ids
+    const uint32_t* pos;      // their positions
+    float* g;
+    float* first;             // [chunks][dim] run that began in an earlier chunk
+    float* last;              // [chunks][dim] run that begins here and goes on
+    int64_t tokens, dim, lddout, ldg;
+    uint32_t vocab, chunks, col_tiles;
+    float scale;
+    int accumulate;
+};
+
+// Eight columns of one row of G.
+__device__ __forceinline__ void put_row(const RunSum& s, uint32_t key, int64_t c, int n, floatx8 acc) {
+    float* p = s.g + (int64_t)key * s.ldg + c;
+    floatx8 v = acc * s.scale;
+    if (s.accumulate) v += Vec8<float>::get(load8_n(p, n));
+    store8_n(p, Vec8<float>::put(v), n);
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
+    const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const uint32_t chunk = wave / s.col_tiles;
+    if (chunk >= s.chunks) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)(wave - chunk * s.col_tiles) * COLS + lane * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, s.dim - c));
+    const int64_t i0 = (int64_t)chunk * CHUNK;
+    const int count = (int)min((int64_t)CHUNK, s.tokens - i0);
+    // lane i < CHUNK holds position i0 + i; lanes CHUNK and CHUNK + 1 the keys on either side
+    uint32_t k = 0xffffffffu, p = 0;
+    if (lane < count) {
+        k = ldg(s.key + i0 + lane);
+        p = ldg(s.pos + i0 + lane);
+    } else if (lane == CHUNK && i0 > 0) {
+        k = ldg(s.key + i0 - 1);
+    } else if (lane == CHUNK + 1 && i0 + CHUNK < s.tokens) {
+        k = ldg(s.key + i0 + CHUNK);
+    }
+    const uint32_t prev = (uint32_t)__builtin_amdgcn_readlane((int)k, CHUNK);
+    const uint32_t next = (uint32_t)__builtin_amdgcn_readlane((int)k, CHUNK + 1);
+    const T* dout = (const T*)s.dout + c;
+    floatx8 acc = {};
+    bool begun_before = (uint32_t)__builtin_amdgcn_readlane((int)k, 0) == prev;
+#pragma unroll
+    for (int b = 0; b < CHUNK; b += 8) {
+        typename Vec8<T>::Raw r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            r[i] = typename Vec8<T>::Raw{};
+            const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
+            const uint32_t row = (uint32_t)__builtin_amdgcn_readlane((int)p, b + i);
+            if (key < s.vocab) r[i] = load8_n(dout + (int64_t)row * s.lddout, n);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
+            if (key >= s.vocab) return;        // tokens without a row come last
+            const uint32_t after = b + i + 1 < CHUNK ? (uint32_t)__builtin_amdgcn_readlane((int)k, (b + i + 1) % 64) : next;
+            acc += Vec8<T>::get(r[i]);
+            const bool at_end = b + i + 1 == CHUNK;
+            if (key != after || at_end) {
+                const bool goes_on = at_end && key == after;
+                if (n > 0) {
+                    if (begun_before)
+                        store8_n(s.first + (int64_t)chunk * s.dim + c, Vec8<float>::put(acc), n);
+                    else if (goes_on)
+                        store8_n(s.last + (int64_t)chunk * s.dim + c, Vec8<float>::put(acc), n);
+                    else
+                        put_row(s, key, c, n, acc);
+                }
+                acc = floatx8{};
+                begun_before = false;
+            }
+        }
+    }
+}
+
+// The run that begins in a chunk and goes on into later ones: its partial rows in order.
+__global__ __launch_bounds__(64 * JOIN_WAVES) void join_runs_kernel(RunSum s) {
+    __shared__ float part[JOIN_WAVES][COLS];
+    const uint32_t chunk = blockIdx.x / s.col_tiles;
+    const int64_t i0 = (int64_t)chunk * CHUNK, i1 = i0 + CHUNK;
+    if (i1 >= s.tokens) return;
+    const uint32_t key = ldg(s.key + i1 - 1);
+    if (key >= s.vocab || ldg(s.key + i1) != key) return;
+    if (ldg(s.key + i0) == key && i0 > 0 && ldg(s.key + i0 - 1) == key) return;    // began before
+    // the run's end: the first sorted position after i1 with another key
+    int64_t lo = i1 + 1, hi = s.tokens;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (ldg(s.key + mid) == key) lo = mid + 1; else hi = mid;
+    }
+    const uint32_t end = (uint32_t)((lo - 1) / CHUNK);      // last chunk of the run
+    const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)(blockIdx.x - chunk * s.col_tiles) * COLS + lane * 8;
+    const int n = (int)max((int64_t)0, min((int64_t)8, s.dim - c));
+    floatx8 acc = {};
+    for (uint32_t j = chunk + wv; j <= end; j += JOIN_WAVES) {
+        const float* p = (j == chunk ? s.last : s.first) + (int64_t)j * s.dim + c;
+        acc += Vec8<float>::get(load8_n(p, n));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[wv][lane * 8 + i] = acc[i];
+    __syncthreads();
+    if (wv == 0 && n > 0) {
+        for (int w = 1; w < JOIN_WAVES; ++w)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += part[w][lane * 8 + i];
+        put_row(s, key, c, n, acc);
+    }
+}
+
+struct GradPlan {
+    int64_t chunks, nblk;
+    int bits, passes, digit, pos_bits;
+    bool small;
+    size_t off_key[2], off_pos[2], off_hist, off_first, off_last, total;
+};
+GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t dim) {
+    GradPlan p;
+    p.chunks = (tokens + CHUNK - 1) / CHUNK;
+    p.bits = bit_length((uint64_t)vocab);                    // keys 0 .. vocab
+    p.passes = (p.bits + RADIX_BITS - 1) / RADIX_BITS;
+    p.digit = (p.bits + p.passes - 1) / p.passes;
+    p.pos_bits = bit_length((uint64_t)(tokens > 0 ? tokens - 1 : 0));
+    // id and position in one word: larger tables sort in blocks, whatever the tokens
+    p.small = tokens <= SMALL_T && p.bits + p.pos_bits <= 32;
+    p.nblk = (tokens + SORT_TILE - 1) / SORT_TILE;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    for (int i = 0; i < 2; ++i) {
+        p.off_key[i] = take((size_t)tokens * 4);
+        p.off_pos[i] = take((size_t)tokens * 4);
+    }
+    p.off_hist = take(p.small ? 0 : (size_t)p.nblk * BINS * 4);
+    p.off_first = take((size_t)p.chunks * dim * 4);
+    p.off_last = take((size_t)p.chunks * dim * 4);
+    p.total = at;
+    return p;
+}
+
+}  // namespace
+
+hipError_t launch_embedding(shampoo4_dtype dtype, const Embed& e, hipStream_t stream) {
+    const uint32_t nvec = (uint32_t)((e.dim + 7) / 8);
+    const uint64_t total = (uint64_t)e.tokens * nvec;
+    if (total == 0) return hipSuccess;
+    const dim3 grid((uint32_t)std::min<uint64_t>((total + 255) / 256, 1u << 20));
+    switch (dtype) {
+        case SHAMPOO4_BF16: S4_LAUNCH(embedding_kernel<__bf16>, grid, dim3(256), 0, stream, e, nvec, total); break;
+        case SHAMPOO4_F16: S4_LAUNCH(embedding_kernel<_Float16>, grid, dim3(256), 0, stream, e, nvec, total); break;
+        default: S4_LAUNCH(embedding_kernel<float>, grid, dim3(256), 0, stream, e, nvec, total);
+    }
+    return hipGetLastError();
+}
+
+size_t embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim) {
+    return grad_plan(tokens, vocab, dim).total;
+}
+
+hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void* workspace, hipStream_t stream) {
+    const GradPlan p = grad_plan(e.tokens, e.vocab, e.dim);
+    char* ws = (char*)workspace;
+    Fill fill{e.accumulate ? nullptr : e.g, e.vocab, e.dim, e.ldg, 0, 1};
+    // workgroups that fill: 8 KB a workgroup and turn, at most four a CU
+    const int64_t fill_bytes = e.accumulate ? 0 : e.vocab * e.dim * 4;
+    const auto fill_blocks = [&](int parts) {
+        return (uint32_t)std::min<int64_t>(1024, (fill_bytes / parts + 8191) / 8192);
+    };
+    uint32_t *skey, *spos;
+    if (e.tokens == 0 && fill_bytes == 0) return hipSuccess;
+    if (e.tokens == 0 || p.small) {
+        skey = (uint32_t*)(ws + p.off_key[0]);
+        spos = (uint32_t*)(ws + p.off_pos[0]);
+        S4_LAUNCH(sort_small_kernel, dim3(1 + fill_blocks(1)), dim3(1024), 0, stream, e.ids, e.id64, e.vocab,
+                  (int)e.tokens, p.passes, p.digit, p.pos_bits, skey, spos, fill);
+    } else {
+        fill.parts = 2 * p.passes;
+        const uint32_t nf = fill_blocks(fill.parts);
+        for (int k = 0; k < p.passes; ++k) {
+            SortPass s;
+            s.ids = k == 0 ? e.ids : nullptr;
+            s.key = (uint32_t*)(ws + p.off_key[(k + 1) & 1]);
+            s.pos = (uint32_t*)(ws + p.off_pos[(k + 1) & 1]);
+            s.key_out = (uint32_t*)(ws + p.off_key[k & 1]);
+            s.pos_out = (uint32_t*)(ws + p.off_pos[k & 1]);
+            s.hist = (uint32_t*)(ws + p.off_hist);
+            s.vocab = e.vocab;
+            s.tokens = e.tokens;
+            s.id64 = e.id64;
+            s.shift = k * p.digit;
+            s.bits = p.digit;
+            s.nblk = (int)p.nblk;
+            fill.part = 2 * k;
+            S4_LAUNCH(sort_count_kernel, dim3((uint32_t)p.nblk + nf), dim3(512), 0, stream, s, fill);
+            fill.part = 2 * k + 1;
+            S4_LAUNCH(sort_scatter_kernel, dim3((uint32_t)p.nblk + nf), dim3(512), 0, stream, s, fill);
+        }
+        skey = (uint32_t*)(ws + p.off_key[(p.passes - 1) & 1]);
+        spos = (uint32_t*)(ws + p.off_pos[(p.passes - 1) & 1]);
+    }
+    if (e.tokens == 0) return hipGetLastError();
+    RunSum r;
+    r.dout = e.dout;
+    r.key = skey;
+    r.pos = spos;
+    r.g = e.g;
+    r.first = (float*)(ws + p.off_first);
+    r.last = (float*)(ws + p.off_last);
+    r.tokens = e.tokens;
+    r.dim = e.dim;
+    r.lddout = e.lddout;
+    r.ldg = e.ldg;
+    r.vocab = (uint32_t)e.vocab;
+    r.chunks = (uint32_t)p.chunks;
+    r.col_tiles = (uint32_t)((e.dim + COLS - 1) / COLS);
+    r.scale = e.scale;
+    r.accumulate = e.accumulate;
+    const uint32_t waves = r.chunks * r.col_tiles;
+    switch (dtype) {
+        case SHAMPOO4_BF16: S4_LAUNCH(run_sums_kernel<__bf16>, dim3((waves + 3) / 4), dim3(256), 0, stream, r); break;
+        case SHAMPOO4_F16: S4_LAUNCH(run_sums_kernel<_Float16>, dim3((waves + 3) / 4), dim3(256), 0, stream, r); break;
+        default: S4_LAUNCH(run_sums_kernel<float>, dim3((waves + 3) / 4), dim3(256), 0, stream, r);
+    }
+    if (r.chunks > 1) S4_LAUNCH(join_runs_kernel, dim3(waves), dim3(64 * JOIN_WAVES), 0, stream, r);
+    return hipGetLastError();
+}
+
+}  // namespace s4

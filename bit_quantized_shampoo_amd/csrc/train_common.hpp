@@ -1,0 +1,161 @@
+// Device-side pieces shared by the training operators: element types, vectors of eight
+// elements at any alignment, and the 8-bit checkpoint's scale and codes.
+#pragma once
+
+#include "common.hpp"
+
+namespace s4 {
+
+typedef float floatx8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Eight consecutive elements as raw bits (`Raw`), and their conversion from and to fp32.
+// The access types are aligned to the element only: gfx950 loads and stores 16 bytes at any
+// element boundary, so odd leading dimensions take the same instructions as even ones.
+template <class T>
+struct Vec8;
+
+template <>
+struct Vec8<__bf16> {
+    typedef u32x4 Raw;
+    typedef u32x4 Mem __attribute__((aligned(2)));
+    static __device__ __forceinline__ floatx8 get(Raw r) {
+        floatx8 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(r[i] << 16);
+            f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+        }
+        return f;
+    }
+    static __device__ __forceinline__ Raw put(floatx8 f) {
+        return __builtin_bit_cast(Raw, __builtin_convertvector(f, bf16x8));
+    }
+};
+template <>
+struct Vec8<_Float16> {
+    typedef u32x4 Raw;
+    typedef u32x4 Mem __attribute__((aligned(2)));
+    static __device__ __forceinline__ floatx8 get(Raw r) {
+        return __builtin_convertvector(__builtin_bit_cast(f16x8, r), floatx8);
+    }
+    static __device__ __forceinline__ Raw put(floatx8 f) {
+        return __builtin_bit_cast(Raw, __builtin_convertvector(f, f16x8));
+    }
+};
+template <>
+struct Vec8<float> {
+    typedef u32x8 Raw;
+    typedef u32x8 Mem __attribute__((aligned(4)));
+    static __device__ __forceinline__ floatx8 get(Raw r) { return __builtin_bit_cast(floatx8, r); }
+    static __device__ __forceinline__ Raw put(floatx8 f) { return __builtin_bit_cast(Raw, f); }
+};
+
+template <class T>
+__device__ __forceinline__ float to_float(T v) { return (float)v; }
+
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::Raw load8(const T* p) {
+    using G = __attribute__((address_space(1))) const typename Vec8<T>::Mem;
+    return *(G*)p;
+}
+template <class T>
+__device__ __forceinline__ void store8(T* p, typename Vec8<T>::Raw v) {
+    using G = __attribute__((address_space(1))) typename Vec8<T>::Mem;
+    *(G*)p = v;
+}
+// The first n (0..8) of eight elements; the others are zero, and not accessed.
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::Raw load8_n(const T* p, int n) {
+    if (n >= 8) return load8(p);
+    typename Vec8<T>::Raw r = {};
+    if constexpr (sizeof(T) == 4) {
+        for (int i = 0; i < n; ++i) {
+            const uint32_t b = ldg((const uint32_t*)p + i);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = i == j ? b : r[j];
+        }
+    } else {
+        for (int i = 0; i < n; ++i) {
+            const uint32_t b = (uint32_t)ldg((const uint16_t*)p + i) << (16 * (i & 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] |= (i >> 1) == j ? b : 0u;
+        }
+    }
+    return r;
+}
+template <class T>
+__device__ __forceinline__ void store8_n(T* p, typename Vec8<T>::Raw v, int n) {
+    if (n >= 8) {
+        store8(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if (i < n) {
+            if constexpr (sizeof(T) == 4)
+                stg((uint32_t*)p + i, v[i]);
+            else
+                stg((uint16_t*)p + i, (uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+        }
+}
+
+// Eight values rounded to T and back: what a consumer of the stored elements reads.
+template <class T>
+__device__ __forceinline__ floatx8 round8(floatx8 f) { return Vec8<T>::get(Vec8<T>::put(f)); }
+
+// -- the 8-bit checkpoint ----------------------------------------------------------------
+
+// Biased exponent e of a block's scale 2^(e - 127), from the bits of its largest |x|
+// (E + mantissa m): a / 2^(E - 6) = 64 m is at most 127 unless the mantissa is above
+// 127/64 = 1 + 0x7e0000 / 2^23, where the added 0x1ffff carries into the exponent.
+__device__ __forceinline__ uint32_t act8_exponent(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return 255u;
+    const int e = (int)((amax_bits + 0x1ffffu) >> 23) - 6;
+    return (uint32_t)max(e, 1);
+}
+__device__ __forceinline__ float act8_scale(uint32_t e) { return __uint_as_float(e << 23); }   // e = 255: infinity
+
+// Codes of eight consecutive columns of one row.  inv = 2^(127 - e): x inv is exact, and
+// adding 1.5 2^23 rounds it to an integer whose two's complement byte is the sum's low
+// byte.  top: 127, or 63 where 64 s is 2^128, or 0 for a block that is not finite.
+struct Act8Block {
+    float inv[8], top[8];
+    __device__ __forceinline__ void set(int j, uint32_t e) {
+        inv[j] = __uint_as_float((254u - min(e, 253u)) << 23);
+        top[j] = e == 255u ? 0.f : e >= 249u ? 63.f : 127.f;
+    }
+    __device__ __forceinline__ u32x2 codes(floatx8 x) const {
+        uint32_t b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // the clamp also turns a NaN into a number (fmaxf returns its other operand)
+            const float y = fminf(fmaxf(x[j] * inv[j], -top[j]), top[j]);
+            b[j] = __float_as_uint(y + 12582912.f);
+        }
+        u32x2 r;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x0c0c0400u);
+            r[h] = lo | hi << 16;
+        }
+        return r;
+    }
+};
+
+// Eight codes times their columns' scales.
+__device__ __forceinline__ floatx8 act8_values(u32x2 c, const float (&s)[8]) {
+    floatx8 f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (float)(int8_t)(c[j >> 2] >> (8 * (j & 3))) * s[j];
+    return f;
+}
+
+__device__ __forceinline__ u32x2 ldg_u2(const void* p) { return ldg((const u32x2*)p); }
+
+}  // namespace s4
