@@ -110,10 +110,8 @@ __device__ __forceinline__ void encode_tile(const typename Vec8<T>::Raw (&r)[8],
     }
 }
 
-__device__ __forceinline__ void load_scales(float (&s)[8], const uint8_t* scales, int64_t pitch, const Tile& t) {
-    const u32x2 p = ldg_u2(scales + t.block * pitch + t.col0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = act8_scale((p[j >> 2] >> (8 * (j & 3))) & 0xffu);
+__device__ __forceinline__ floatx8 load_scales(const uint8_t* scales, int64_t pitch, const Tile& t) {
+    return act8_scales(ldg_u2(scales + t.block * pitch + t.col0));
 }
 
 template <class T>
@@ -151,8 +149,7 @@ __global__ __launch_bounds__(256) void act8_load_kernel(Act8Ptr in, T* __restric
     u32x2 q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = ldg_u2(c + i * pitch);     // padded rows and columns exist
-    float s[8];
-    load_scales(s, in.scales, pitch, t);
+    const floatx8 s = load_scales(in.scales, pitch, t);
     typename Vec8<T>::Raw r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = Vec8<T>::put(saturate<T>(act8_values(q[i], s)));
@@ -215,9 +212,9 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int64_
     }
     typename Vec8<T>::Raw d[8], du[8];
     load_tile(d, (const T*)a.dh, a.lddh, t, full);
-    float sg[8], su[8];
-    load_scales(sg, a.gate8.scales, pitch, t);
-    if constexpr (GATED) load_scales(su, a.up8.scales, pitch, t);
+    const floatx8 sg = load_scales(a.gate8.scales, pitch, t);
+    floatx8 su;
+    if constexpr (GATED) su = load_scales(a.up8.scales, pitch, t);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const floatx8 x = act8_values(cg[i], sg);

@@ -148,11 +148,58 @@ struct Act8Block {
     }
 };
 
-// Eight codes times their columns' scales.
-__device__ __forceinline__ floatx8 act8_values(u32x2 c, const float (&s)[8]) {
+// Byte B of a register as a signed number, and shifted into a scale: one instruction each
+// (the byte is picked and extended by the instruction's operand selection).
+template <int B>
+__device__ __forceinline__ float code_value(uint32_t c) {
+    float f;
+    if constexpr (B == 0)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_0" : "=v"(f) : "v"(c));
+    else if constexpr (B == 1)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_1" : "=v"(f) : "v"(c));
+    else if constexpr (B == 2)
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_2" : "=v"(f) : "v"(c));
+    else
+        asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_3" : "=v"(f) : "v"(c));
+    return f;
+}
+template <int B>
+__device__ __forceinline__ float byte_scale(uint32_t e) {
+    float f;
+    const uint32_t sh = 23;
+    if constexpr (B == 0)
+        asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_0" : "=v"(f) : "v"(sh), "v"(e));
+    else if constexpr (B == 1)
+        asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_1" : "=v"(f) : "v"(sh), "v"(e));
+    else if constexpr (B == 2)
+        asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_2" : "=v"(f) : "v"(sh), "v"(e));
+    else
+        asm("v_lshlrev_b32_sdwa %0, %1, %2 dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:DWORD src1_sel:BYTE_3" : "=v"(f) : "v"(sh), "v"(e));
+    return f;
+}
+// The scales of eight columns from their exponents, and eight codes times them.
+__device__ __forceinline__ floatx8 act8_scales(u32x2 e) {
+    floatx8 s;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        s[4 * h] = byte_scale<0>(e[h]);
+        s[4 * h + 1] = byte_scale<1>(e[h]);
+        s[4 * h + 2] = byte_scale<2>(e[h]);
+        s[4 * h + 3] = byte_scale<3>(e[h]);
+    }
+    return s;
+}
+__device__ __forceinline__ floatx8 act8_values(u32x2 c, floatx8 s) {
     floatx8 f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = (float)(int8_t)(c[j >> 2] >> (8 * (j & 3))) * s[j];
+    for (int h = 0; h < 2; ++h) {
+        f[4 * h] = code_value<0>(c[h]);
+        f[4 * h + 1] = code_value<1>(c[h]);
+        f[4 * h + 2] = code_value<2>(c[h]);
+        f[4 * h + 3] = code_value<3>(c[h]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= s[j];
     return f;
 }
 

@@ -18,13 +18,6 @@ namespace {
 
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 
-constexpr int BM = 128, BN = 128;            // output tile: channels of dY x channels of X
-constexpr int KS = 32;                       // tokens a slice: one block of the checkpoint
-constexpr int PITCH = 160;                   // LDS row pitch in bf16: 320 bytes, so the four
-                                             // token rows of a transposing read are 64 bytes
-                                             // apart modulo the 256 bytes of the banks
-constexpr int THREADS = 256;                 // 2 x 2 waves of 64 x 64
-
 template <class T>
 struct Pieces;
 template <>
@@ -52,6 +45,11 @@ __device__ __forceinline__ u32x4 take_piece(floatx8& f) {
     return p;
 }
 
+// LDS row pitch in bf16 of a tile `cols` wide: the four token rows that a group of sixteen
+// lanes reads at once start 64 bytes apart modulo the 256 bytes of the banks, beside the other group's.
+constexpr int tile_pitch(int cols) { return cols + 32; }
+
+// Eight values of one token into the pieces' planes.
 template <class T>
 __device__ __forceinline__ void split_store(uint16_t* lds, int plane, int at, typename Vec8<T>::Raw r) {
     if constexpr (Pieces<T>::N == 1) {
@@ -64,6 +62,7 @@ __device__ __forceinline__ void split_store(uint16_t* lds, int plane, int at, ty
 }
 
 // Eight consecutive tokens (k0 + 8 (lane / 32) ..) of column n0 + lane % 32.
+template <int PITCH>
 __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int k0, int n0) {
     const int lane = threadIdx.x & 63;
     const uint16_t* p = lds + (k0 + (lane >> 5) * 8 + ((lane >> 2) & 3)) * PITCH + n0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
@@ -74,71 +73,183 @@ __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int k0, int n0) 
     return u.v;
 }
 
-template <class T>
-__global__ __launch_bounds__(THREADS) void wgrad_kernel(WGrad w, int tiles_m, int64_t rows_per, bool partial) {
-    constexpr int NP = Pieces<T>::N;
-    constexpr int PLANE = KS * PITCH;
-    __shared__ uint16_t lds[(NP + 1) * PLANE];
-    uint16_t* la = lds;
-    uint16_t* lb = lds + NP * PLANE;
+// A workgroup of WM x WN waves, each with TM x TN blocks of 32 x 32; slices of KS tokens.
+template <class T, int WM, int WN, int TM, int TN, int KS>
+struct Shape {
+    static constexpr int BM = WM * TM * 32, BN = WN * TN * 32, THREADS = 64 * WM * WN;
+    static constexpr int NP = Pieces<T>::N;
+    static constexpr int PA = tile_pitch(BM), PB = tile_pitch(BN);
+    static constexpr int PLANE = KS * PA;                    // one piece of dY
+    static constexpr int STAGE = NP * PLANE + KS * PB;       // bf16 elements of a stage
+    static constexpr int STEPS = KS / 16;                    // matrix-core steps of a slice
+    static constexpr int VA = KS * BM / 8 / THREADS;         // vectors of dY a thread stages
+    static constexpr int VB = KS * BN / 8 / THREADS;         // vectors of codes
+    static constexpr size_t LDS_BYTES = 2 * STAGE * 2;
+    // a thread's code vectors share their columns and their block of 32 tokens
+    static_assert(VA % STEPS == 0 && VB % STEPS == 0, "stage parts");
+    static_assert(THREADS % (BM / 8) == 0 && THREADS % (BN / 8) == 0, "columns fixed per thread");
+};
+
+template <class T, int WM, int WN, int TM, int TN, int KS>
+__global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_m, int tiles_n, int64_t rows_per,
+                                                             bool partial) {
+    using S = Shape<T, WM, WN, TM, TN, KS>;
+    using Raw = typename Vec8<T>::Raw;
+    constexpr int THREADS = S::THREADS, STEPS = S::STEPS, VA = S::VA, VB = S::VB;
+    extern __shared__ uint16_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int tile_m = blockIdx.x % tiles_m, tile_n = blockIdx.x / tiles_m;
-    const int64_t m0 = (int64_t)tile_m * BM, n0 = (int64_t)tile_n * BN;
+    const int64_t m0 = (int64_t)tile_m * S::BM, n0 = (int64_t)tile_n * S::BN;
     const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(w.rows, r0 + rows_per);
     const int64_t pitch = act8_pitch(w.cols);
-    // staging: thread (row, seg) takes 16 consecutive columns of one token of each tile
-    const int srow = tid >> 3, seg = (tid & 7) * 16;
-    const int64_t am = m0 + seg, bn = n0 + seg;
-    const int an = (int)max((int64_t)0, min((int64_t)16, w.n - am));
-    const bool bok = bn < pitch;
-    const int wm = (wv & 1) * 64, wn = (wv >> 1) * 64;
-    floatx16 acc[2][2] = {};
-    for (int64_t k = r0; k < r1; k += KS) {
-        typename Vec8<T>::Raw a[2] = {};
-        u32x4 c = {}, e = {};
-        if (k + srow < r1) {
-            const T* p = (const T*)w.dy + (k + srow) * w.lddy + am;
-            a[0] = load8_n(p, an);
-            a[1] = load8_n(p + 8, max(0, an - 8));
-        }
-        if (bok) {
-            c = ldg((const u32x4*)(w.codes + (k + srow) * pitch + bn));
-            e = ldg((const u32x4*)(w.scales + (k / 32) * pitch + bn));
-        }
+    const int wm = (wv % WM) * TM * 32, wn = (wv / WM) * TN * 32;
+
+    // staging: thread (row, column group) of both tiles; its vectors are AR (BR) rows apart
+    constexpr int AR = THREADS / (S::BM / 8), BR = THREADS / (S::BN / 8);
+    const int arow = tid / (S::BM / 8), acol = tid % (S::BM / 8) * 8;
+    const int brow = tid / (S::BN / 8), bcol = tid % (S::BN / 8) * 8;
+    const int64_t bn = min(n0 + bcol, pitch - 8);            // beyond: columns that are not stored
+    // addresses: a base that the workgroup shares (scalar registers) and 32-bit lane offsets
+    const char* pa = (const char*)((const T*)w.dy + r0 * w.lddy + m0);
+    const char* pc = (const char*)w.codes + r0 * pitch;
+    const char* pe = (const char*)w.scales + r0 / 32 * pitch;
+    const uint32_t oa = (uint32_t)((arow * w.lddy + acol) * sizeof(T));
+    const uint32_t oe = (uint32_t)bn, oc = (uint32_t)(brow * pitch + bn);
+    const int64_t sa = AR * w.lddy * (int64_t)sizeof(T), sc = BR * pitch;
+
+    Raw a[VA];
+    u32x2 c[VB], e[KS / 32];
+    const auto store_a = [&](int buf, int i) {
+        split_store<T>(lds + buf * S::STAGE, S::PLANE, (arow + i * AR) * S::PA + acol, a[i]);
+    };
+    const auto store_b = [&](int buf, int i) {
+        // opaque: taken apart where it is loaded, the codes would be waited for there
+        asm volatile("" : "+v"(c[i]), "+v"(e[i * BR / 32]));
+        const floatx8 v = act8_values(c[i], act8_scales(e[i * BR / 32]));
+        u32x4 q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = pack_hi(v[2 * j], v[2 * j + 1]);
+        *(u32x4*)(lds + buf * S::STAGE + S::NP * S::PLANE + (brow + i * BR) * S::PB + bcol) = q;
+    };
+
+    floatx16 acc[TM][TN] = {};
+    struct Frags {
+        bf16x8 a[S::NP][TM], b[TN];
+    };
+    const auto read_frags = [&](Frags& f, int buf, int ks) {
+        const uint16_t* la = lds + buf * S::STAGE;
+        const uint16_t* lb = la + S::NP * S::PLANE;
+#pragma unroll
+        for (int n = 0; n < TN; ++n) f.b[n] = fragment<S::PB>(lb, 16 * ks, wn + 32 * n);
+#pragma unroll
+        for (int q = 0; q < S::NP; ++q)
+#pragma unroll
+            for (int m = 0; m < TM; ++m) f.a[q][m] = fragment<S::PA>(la + q * S::PLANE, 16 * ks, wm + 32 * m);
+    };
+    const auto products = [&](const Frags& f) {
+#pragma unroll
+        for (int q = 0; q < S::NP; ++q)
+#pragma unroll
+            for (int m = 0; m < TM; ++m)
+#pragma unroll
+                for (int n = 0; n < TN; ++n)
+                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q][m], f.b[n], acc[m][n], 0, 0, 0);
+    };
+
+    // Whole slices whose loads all lie inside dY.  A load past a row's end reads the start of
+    // the next row, into columns of G that are not stored; only the last rows need care.
+    int64_t fast = 0;
+    {
+        const int64_t x = (w.rows - 1) * w.lddy + w.n - m0 - S::BM;    // last row start that may be loaded
+        const int64_t k = x >= 0 ? x / w.lddy - (KS - 1) : -1;         // last slice start
+        // lane offsets of 32 bits: AR (BR) rows
+        const bool narrow = w.lddy < (1 << 24) && pitch < (1 << 24);
+        if (narrow && k >= r0 && r1 > r0) fast = min((r1 - r0) / KS, (k - r0) / KS + 1);
+    }
+    if (fast > 0) {
+        const auto shared_base = [](const char* p) {
+            asm("" : "+s"(p));
+            return p;
+        };
+        const auto load_a = [&](int64_t slice, int i) { a[i] = load8((const T*)(shared_base(pa + (slice * VA + i) * sa) + oa)); };
+        const auto load_b = [&](int64_t slice, int i) { c[i] = ldg((const u32x2*)(shared_base(pc + (slice * VB + i) * sc) + oc)); };
+        const auto load_e = [&](int64_t slice, int i) { e[i] = ldg((const u32x2*)(shared_base(pe + (slice * (KS / 32) + i) * pitch) + oe)); };
+        // the scales of a block of 32 tokens follow its last codes
+        constexpr int PER_E = 32 / BR;
+#pragma unroll
+        for (int i = 0; i < VA; ++i) load_a(0, i);
+#pragma unroll
+        for (int i = 0; i < VB; ++i) load_b(0, i);
+#pragma unroll
+        for (int i = 0; i < KS / 32; ++i) load_e(0, i);
+        const auto stage = [&](int buf, int64_t next, int i0a, int i1a, int i0b, int i1b) {
+#pragma unroll
+            for (int i = i0a; i < i1a; ++i) {
+                store_a(buf, i);
+                load_a(next, i);
+            }
+#pragma unroll
+            for (int i = i0b; i < i1b; ++i) {
+                store_b(buf, i);
+                load_b(next, i);
+                if ((i + 1) % PER_E == 0) load_e(next, i / PER_E);
+            }
+        };
+        stage(0, min<int64_t>(1, fast - 1), 0, VA, 0, VB);
         __syncthreads();
-        split_store<T>(la, PLANE, srow * PITCH + seg, a[0]);
-        split_store<T>(la, PLANE, srow * PITCH + seg + 8, a[1]);
+        for (int64_t s = 0; s < fast; ++s) {
+            const int buf = (int)s & 1;
+            const int64_t next = min(s + 2, fast - 1);
+            Frags f[2];
+            read_frags(f[0], buf, 0);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float s[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s[j] = act8_scale((e[2 * h + (j >> 2)] >> (8 * (j & 3))) & 0xffu);
-            const floatx8 x = act8_values(u32x2{c[2 * h], c[2 * h + 1]}, s);
-            u32x4 p;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = pack_hi(x[2 * j], x[2 * j + 1]);
-            *(u32x4*)(lb + srow * PITCH + seg + 8 * h) = p;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int ks = 0; ks < KS; ks += 16) {
-            const bf16x8 b0 = fragment(lb, ks, wn), b1 = fragment(lb, ks, wn + 32);
-#pragma unroll
-            for (int q = 0; q < NP; ++q)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const bf16x8 av = fragment(la + q * PLANE, ks, wm + 32 * m);
-                    acc[m][0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, b0, acc[m][0], 0, 0, 0);
-                    acc[m][1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(av, b1, acc[m][1], 0, 0, 0);
-                }
+            for (int ks = 0; ks < STEPS; ++ks) {
+                if (ks + 1 < STEPS) read_frags(f[(ks + 1) & 1], buf, ks + 1);
+                products(f[ks & 1]);
+                // a part of the next slice to the other stage, and of the one after it on its way
+                stage(buf ^ 1, next, ks * (VA / STEPS), (ks + 1) * (VA / STEPS), ks * (VB / STEPS), (ks + 1) * (VB / STEPS));
+                // without this the loads gather at the slice's end and are waited for at once
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            __syncthreads();
         }
     }
+    // What is left: the last rows, with every load checked.
+    for (int64_t k = r0 + fast * KS; k < r1; k += KS) {
+#pragma unroll
+        for (int i = 0; i < VA; ++i) {
+            const int64_t row = k + arow + i * AR;
+            const int n = (int)max((int64_t)0, min((int64_t)8, w.n - m0 - acol));
+            a[i] = load8_n((const T*)w.dy + row * w.lddy + m0 + acol, row < r1 ? n : 0);
+        }
+#pragma unroll
+        for (int i = 0; i < KS / 32; ++i) e[i] = k + 32 * i < r1 ? ldg((const u32x2*)(w.scales + (k / 32 + i) * pitch + bn)) : u32x2{0, 0};
+#pragma unroll
+        for (int i = 0; i < VB; ++i) {
+            const int64_t row = k + brow + i * BR;
+            c[i] = u32x2{0, 0};
+            if (row < r1) c[i] = ldg((const u32x2*)(w.codes + row * pitch + bn));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VA; ++i) store_a(0, i);
+#pragma unroll
+        for (int i = 0; i < VB; ++i) store_b(0, i);
+        __syncthreads();
+#pragma unroll
+        for (int ks = 0; ks < STEPS; ++ks) {
+            Frags f;
+            read_frags(f, 0, ks);
+            products(f);
+        }
+    }
+
     float* out = partial ? w.parts + (int64_t)blockIdx.y * w.n * w.cols : w.g;
     const int64_t ld = partial ? w.cols : w.ldg;
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int m = 0; m < TM; ++m)
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < TN; ++n)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int64_t row = m0 + wm + 32 * m + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
@@ -165,18 +276,39 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(WGrad w, int splits) {
 }
 
 struct WPlan {
+    bool large;               // 256 x 256 tiles, else 128 x 128
     int64_t tiles_m, tiles_n, rows_per;
     int splits;
 };
 WPlan wgrad_plan(int64_t rows, int64_t n, int64_t cols) {
     WPlan p;
-    p.tiles_m = (n + BM - 1) / BM;
-    p.tiles_n = (cols + BN - 1) / BN;
+    p.large = ((n + 255) / 256) * ((cols + 255) / 256) >= 128;
+    const int64_t tile = p.large ? 256 : 128;
+    p.tiles_m = (n + tile - 1) / tile;
+    p.tiles_n = (cols + tile - 1) / tile;
     const int64_t tiles = p.tiles_m * p.tiles_n;
-    int64_t s = std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), rows / 256));
-    p.rows_per = ((rows + s - 1) / s + KS - 1) / KS * KS;
+    const int64_t s = p.large ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), rows / 256));
+    p.rows_per = ((rows + s - 1) / s + 63) / 64 * 64;
     p.splits = rows > 0 ? (int)((rows + p.rows_per - 1) / p.rows_per) : 1;
     return p;
+}
+
+template <class T, int WM, int WN, int TM, int TN, int KS>
+hipError_t wgrad_launch(const WGrad& w, const WPlan& p, hipStream_t stream) {
+    using S = Shape<T, WM, WN, TM, TN, KS>;
+    static const hipError_t attr = hipFuncSetAttribute((const void*)wgrad_kernel<T, WM, WN, TM, TN, KS>,
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS_BYTES);
+    if (attr != hipSuccess) return attr;
+    S4_LAUNCH((wgrad_kernel<T, WM, WN, TM, TN, KS>), dim3((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)p.splits),
+              dim3(S::THREADS), S::LDS_BYTES, stream, w, (int)p.tiles_m, (int)p.tiles_n, p.rows_per, p.splits > 1);
+    return hipSuccess;
+}
+
+template <class T>
+hipError_t wgrad_of(const WGrad& w, const WPlan& p, hipStream_t stream) {
+    // three pieces of a 64-token slice would not fit twice into LDS
+    constexpr int KS = Pieces<T>::N == 1 ? 64 : 32;
+    return p.large ? wgrad_launch<T, 2, 4, 4, 2, KS>(w, p, stream) : wgrad_launch<T, 2, 2, 2, 2, 32>(w, p, stream);
 }
 
 }  // namespace
@@ -189,13 +321,14 @@ size_t wgrad_workspace_bytes(int64_t rows, int64_t n, int64_t cols) {
 hipError_t launch_wgrad(shampoo4_dtype dtype, const WGrad& w, hipStream_t stream) {
     if (w.n <= 0 || w.cols <= 0) return hipSuccess;
     const WPlan p = wgrad_plan(w.rows, w.n, w.cols);
-    const dim3 grid((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)p.splits);
     const bool part = p.splits > 1;
+    hipError_t e;
     switch (dtype) {
-        case SHAMPOO4_BF16: S4_LAUNCH(wgrad_kernel<__bf16>, grid, dim3(THREADS), 0, stream, w, (int)p.tiles_m, p.rows_per, part); break;
-        case SHAMPOO4_F16: S4_LAUNCH(wgrad_kernel<_Float16>, grid, dim3(THREADS), 0, stream, w, (int)p.tiles_m, p.rows_per, part); break;
-        default: S4_LAUNCH(wgrad_kernel<float>, grid, dim3(THREADS), 0, stream, w, (int)p.tiles_m, p.rows_per, part);
+        case SHAMPOO4_BF16: e = wgrad_of<__bf16>(w, p, stream); break;
+        case SHAMPOO4_F16: e = wgrad_of<_Float16>(w, p, stream); break;
+        default: e = wgrad_of<float>(w, p, stream);
     }
+    if (e != hipSuccess) return e;
     if (part) {
         const dim3 sg((uint32_t)std::min<int64_t>((w.n * w.cols + 255) / 256, 4096));
         S4_LAUNCH(wgrad_sum_kernel, sg, dim3(256), 0, stream, w, p.splits);
