@@ -85,10 +85,27 @@ struct Shape {
     static constexpr int VA = KS * BM / 8 / THREADS;         // vectors of dY a thread stages
     static constexpr int VB = KS * BN / 8 / THREADS;         // vectors of codes
     static constexpr size_t LDS_BYTES = 2 * STAGE * 2;
-    // a thread's code vectors share their columns and their block of 32 tokens
-    static_assert(VA % STEPS == 0 && VB % STEPS == 0, "stage parts");
     static_assert(THREADS % (BM / 8) == 0 && THREADS % (BN / 8) == 0, "columns fixed per thread");
 };
+
+// Row range and output tile of this workgroup.  Workgroups go to the eight XCDs round robin;
+// each XCD takes a contiguous range of the tiles (the remainder, under eight, keeps its
+// place), ordered in groups of four tile rows.  The tiles that one L2 serves are then a
+// compact region: they share their columns of dY and X, and their neighbouring columns
+// spread over the L2's channels where a power-of-two row length would fold a single
+// column of tiles onto a few of them.
+__device__ __forceinline__ void place(int tiles_m, int tiles_n, int& split, int& tile_m, int& tile_n) {
+    const int n = gridDim.x, n8 = n >> 3;
+    const int b = (int)blockIdx.x < 8 * n8 ? ((int)blockIdx.x & 7) * n8 + ((int)blockIdx.x >> 3) : (int)blockIdx.x;
+    const int tiles = tiles_m * tiles_n;
+    split = b / tiles;
+    const int t = b - split * tiles;
+    const int g = t / (4 * tiles_n);
+    const int gh = min(4, tiles_m - 4 * g);
+    const int local = t - 4 * g * tiles_n;
+    tile_m = 4 * g + local % gh;
+    tile_n = local / gh;
+}
 
 template <class T, int WM, int WN, int TM, int TN, int KS>
 __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_m, int tiles_n, int64_t rows_per,
@@ -98,9 +115,10 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
     constexpr int THREADS = S::THREADS, STEPS = S::STEPS, VA = S::VA, VB = S::VB;
     extern __shared__ uint16_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int tile_m = blockIdx.x % tiles_m, tile_n = blockIdx.x / tiles_m;
+    int split, tile_m, tile_n;
+    place(tiles_m, tiles_n, split, tile_m, tile_n);
     const int64_t m0 = (int64_t)tile_m * S::BM, n0 = (int64_t)tile_n * S::BN;
-    const int64_t r0 = (int64_t)blockIdx.y * rows_per, r1 = min(w.rows, r0 + rows_per);
+    const int64_t r0 = (int64_t)split * rows_per, r1 = min(w.rows, r0 + rows_per);
     const int64_t pitch = act8_pitch(w.cols);
     const int wm = (wv % WM) * TM * 32, wn = (wv / WM) * TN * 32;
 
@@ -197,22 +215,27 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
         };
         stage(0, min<int64_t>(1, fast - 1), 0, VA, 0, VB);
         __syncthreads();
+        Frags f[2];
+        read_frags(f[0], 0, 0);
         for (int64_t s = 0; s < fast; ++s) {
             const int buf = (int)s & 1;
             const int64_t next = min(s + 2, fast - 1);
-            Frags f[2];
-            read_frags(f[0], buf, 0);
 #pragma unroll
             for (int ks = 0; ks < STEPS; ++ks) {
-                if (ks + 1 < STEPS) read_frags(f[(ks + 1) & 1], buf, ks + 1);
+                // The next slice is whole in LDS before the last step, and this slice's last
+                // operands are in registers: the one barrier of a slice, with products to
+                // follow it while the next operands are read.
+                if (ks == STEPS - 1) __syncthreads();
+                read_frags(f[(ks + 1) & 1], ks == STEPS - 1 ? buf ^ 1 : buf, (ks + 1) % STEPS);
                 products(f[ks & 1]);
                 // a part of the next slice to the other stage, and of the one after it on its way
-                stage(buf ^ 1, next, ks * (VA / STEPS), (ks + 1) * (VA / STEPS), ks * (VB / STEPS), (ks + 1) * (VB / STEPS));
+                constexpr int P = STEPS - 1;
+                if (ks < P) stage(buf ^ 1, next, ks * VA / P, (ks + 1) * VA / P, ks * VB / P, (ks + 1) * VB / P);
                 // without this the loads gather at the slice's end and are waited for at once
                 __builtin_amdgcn_sched_barrier(0);
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
     // What is left: the last rows, with every load checked.
     for (int64_t k = r0 + fast * KS; k < r1; k += KS) {
@@ -244,7 +267,7 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
         }
     }
 
-    float* out = partial ? w.parts + (int64_t)blockIdx.y * w.n * w.cols : w.g;
+    float* out = partial ? w.parts + (int64_t)split * w.n * w.cols : w.g;
     const int64_t ld = partial ? w.cols : w.ldg;
 #pragma unroll
     for (int m = 0; m < TM; ++m)
@@ -299,7 +322,7 @@ hipError_t wgrad_launch(const WGrad& w, const WPlan& p, hipStream_t stream) {
     static const hipError_t attr = hipFuncSetAttribute((const void*)wgrad_kernel<T, WM, WN, TM, TN, KS>,
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS_BYTES);
     if (attr != hipSuccess) return attr;
-    S4_LAUNCH((wgrad_kernel<T, WM, WN, TM, TN, KS>), dim3((uint32_t)(p.tiles_m * p.tiles_n), (uint32_t)p.splits),
+    S4_LAUNCH((wgrad_kernel<T, WM, WN, TM, TN, KS>), dim3((uint32_t)(p.tiles_m * p.tiles_n * p.splits)),
               dim3(S::THREADS), S::LDS_BYTES, stream, w, (int)p.tiles_m, (int)p.tiles_n, p.rows_per, p.splits > 1);
     return hipSuccess;
 }
