@@ -45,9 +45,14 @@ __device__ __forceinline__ u32x4 take_piece(floatx8& f) {
     return p;
 }
 
-// LDS row pitch in bf16 of a tile `cols` wide: the four token rows that a group of sixteen
-// lanes reads at once start 64 bytes apart modulo the 256 bytes of the banks, beside the other group's.
-constexpr int tile_pitch(int cols) { return cols + 32; }
+// Place in LDS of column `col` (a multiple of 4) of token `row`, in bf16, for a tile `cols`
+// wide: rows are dense, and the 64-byte blocks of a row change places by the row's number
+// modulo 4.  The four token rows that a transposing read takes at once (64 bytes of each, for
+// half a wave) then lie in different quarters of the 256 bytes of the banks.
+template <int COLS>
+__device__ __forceinline__ int lds_at(int row, int col) {
+    return row * COLS + (col ^ ((row & 3) << 5));
+}
 
 // Eight values of one token into the pieces' planes.
 template <class T>
@@ -61,15 +66,17 @@ __device__ __forceinline__ void split_store(uint16_t* lds, int plane, int at, ty
     }
 }
 
-// Eight consecutive tokens (k0 + 8 (lane / 32) ..) of column n0 + lane % 32.
-template <int PITCH>
+// Eight consecutive tokens (k0 + 8 (lane / 32) ..) of column n0 + lane % 32 (k0 a multiple of
+// 16, n0 of 32).
+template <int COLS>
 __device__ __forceinline__ bf16x8 fragment(const uint16_t* lds, int k0, int n0) {
     const int lane = threadIdx.x & 63;
-    const uint16_t* p = lds + (k0 + (lane >> 5) * 8 + ((lane >> 2) & 3)) * PITCH + n0 + ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    const int row = (lane >> 5) * 8 + ((lane >> 2) & 3), col = ((lane >> 4) & 1) * 16 + (lane & 3) * 4;
+    const uint16_t* p = lds + k0 * COLS + lds_at<COLS>(row, n0 + col);
     using L = __attribute__((address_space(3))) shortx4;
     union { shortx4 s[2]; bf16x8 v; } u;
     u.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)p);
-    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + 4 * PITCH));
+    u.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L*)(p + 4 * COLS));
     return u.v;
 }
 
@@ -78,13 +85,13 @@ template <class T, int WM, int WN, int TM, int TN, int KS>
 struct Shape {
     static constexpr int BM = WM * TM * 32, BN = WN * TN * 32, THREADS = 64 * WM * WN;
     static constexpr int NP = Pieces<T>::N;
-    static constexpr int PA = tile_pitch(BM), PB = tile_pitch(BN);
-    static constexpr int PLANE = KS * PA;                    // one piece of dY
-    static constexpr int STAGE = NP * PLANE + KS * PB;       // bf16 elements of a stage
+    static constexpr int PLANE = KS * BM;                    // one piece of dY
+    static constexpr int STAGE_A = NP * PLANE, STAGE_B = KS * BN;    // bf16 elements of a stage
     static constexpr int STEPS = KS / 16;                    // matrix-core steps of a slice
+    static constexpr int UNITS = STEPS * NP;                 // of one piece of dY each
     static constexpr int VA = KS * BM / 8 / THREADS;         // vectors of dY a thread stages
     static constexpr int VB = KS * BN / 8 / THREADS;         // vectors of codes
-    static constexpr size_t LDS_BYTES = 2 * STAGE * 2;
+    static constexpr size_t LDS_BYTES = 2 * (STAGE_A + STAGE_B) * 2;
     static_assert(THREADS % (BM / 8) == 0 && THREADS % (BN / 8) == 0, "columns fixed per thread");
 };
 
@@ -112,7 +119,7 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
                                                              bool partial) {
     using S = Shape<T, WM, WN, TM, TN, KS>;
     using Raw = typename Vec8<T>::Raw;
-    constexpr int THREADS = S::THREADS, STEPS = S::STEPS, VA = S::VA, VB = S::VB;
+    constexpr int THREADS = S::THREADS, VA = S::VA, VB = S::VB;
     extern __shared__ uint16_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     int split, tile_m, tile_n;
@@ -127,18 +134,15 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
     const int arow = tid / (S::BM / 8), acol = tid % (S::BM / 8) * 8;
     const int brow = tid / (S::BN / 8), bcol = tid % (S::BN / 8) * 8;
     const int64_t bn = min(n0 + bcol, pitch - 8);            // beyond: columns that are not stored
-    // addresses: a base that the workgroup shares (scalar registers) and 32-bit lane offsets
-    const char* pa = (const char*)((const T*)w.dy + r0 * w.lddy + m0);
-    const char* pc = (const char*)w.codes + r0 * pitch;
-    const char* pe = (const char*)w.scales + r0 / 32 * pitch;
+    // 32-bit lane offsets, beside bases that the workgroup shares (in scalar registers)
     const uint32_t oa = (uint32_t)((arow * w.lddy + acol) * sizeof(T));
     const uint32_t oe = (uint32_t)bn, oc = (uint32_t)(brow * pitch + bn);
     const int64_t sa = AR * w.lddy * (int64_t)sizeof(T), sc = BR * pitch;
 
-    Raw a[VA];
+    Raw a[VA];                                               // this thread's part of a slice
     u32x2 c[VB], e[KS / 32];
     const auto store_a = [&](int buf, int i) {
-        split_store<T>(lds + buf * S::STAGE, S::PLANE, (arow + i * AR) * S::PA + acol, a[i]);
+        split_store<T>(lds + buf * S::STAGE_A, S::PLANE, lds_at<S::BM>(arow + i * AR, acol), a[i]);
     };
     const auto store_b = [&](int buf, int i) {
         // opaque: taken apart where it is loaded, the codes would be waited for there
@@ -147,31 +151,29 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
         u32x4 q;
 #pragma unroll
         for (int j = 0; j < 4; ++j) q[j] = pack_hi(v[2 * j], v[2 * j + 1]);
-        *(u32x4*)(lds + buf * S::STAGE + S::NP * S::PLANE + (brow + i * BR) * S::PB + bcol) = q;
+        *(u32x4*)(lds + 2 * S::STAGE_A + buf * S::STAGE_B + lds_at<S::BN>(brow + i * BR, bcol)) = q;
     };
 
     floatx16 acc[TM][TN] = {};
-    struct Frags {
-        bf16x8 a[S::NP][TM], b[TN];
+    // Operands of a unit (one step of 16 tokens, one piece of dY), double buffered: the next
+    // unit's are read while this one's products run.
+    bf16x8 fa[2][TM], fb[2][TN];
+    const auto read_unit = [&](int buf, int u) {
+        const uint16_t* la = lds + buf * S::STAGE_A + u % S::NP * S::PLANE;
+        const uint16_t* lb = lds + 2 * S::STAGE_A + buf * S::STAGE_B;
+        const int ks = u / S::NP;
+        if (u % S::NP == 0)
+#pragma unroll
+            for (int n = 0; n < TN; ++n) fb[ks & 1][n] = fragment<S::BN>(lb, 16 * ks, wn + 32 * n);
+#pragma unroll
+        for (int m = 0; m < TM; ++m) fa[u & 1][m] = fragment<S::BM>(la, 16 * ks, wm + 32 * m);
     };
-    const auto read_frags = [&](Frags& f, int buf, int ks) {
-        const uint16_t* la = lds + buf * S::STAGE;
-        const uint16_t* lb = la + S::NP * S::PLANE;
+    const auto products = [&](int u) {
 #pragma unroll
-        for (int n = 0; n < TN; ++n) f.b[n] = fragment<S::PB>(lb, 16 * ks, wn + 32 * n);
+        for (int m = 0; m < TM; ++m)
 #pragma unroll
-        for (int q = 0; q < S::NP; ++q)
-#pragma unroll
-            for (int m = 0; m < TM; ++m) f.a[q][m] = fragment<S::PA>(la + q * S::PLANE, 16 * ks, wm + 32 * m);
-    };
-    const auto products = [&](const Frags& f) {
-#pragma unroll
-        for (int q = 0; q < S::NP; ++q)
-#pragma unroll
-            for (int m = 0; m < TM; ++m)
-#pragma unroll
-                for (int n = 0; n < TN; ++n)
-                    acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[q][m], f.b[n], acc[m][n], 0, 0, 0);
+            for (int n = 0; n < TN; ++n)
+                acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[u & 1][m], fb[u / S::NP & 1][n], acc[m][n], 0, 0, 0);
     };
 
     // Whole slices whose loads all lie inside dY.  A load past a row's end reads the start of
@@ -185,55 +187,79 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
         if (narrow && k >= r0 && r1 > r0) fast = min((r1 - r0) / KS, (k - r0) / KS + 1);
     }
     if (fast > 0) {
-        const auto shared_base = [](const char* p) {
+        using Global = __attribute__((address_space(1))) const char;
+        Global* na = (Global*)((const T*)w.dy + r0 * w.lddy + m0);       // the slice to load next
+        Global* nc = (Global*)(w.codes + r0 * pitch);
+        Global* ne = (Global*)(w.scales + r0 / 32 * pitch);
+        const auto base = [](Global* p) {
             asm("" : "+s"(p));
             return p;
         };
-        const auto load_a = [&](int64_t slice, int i) { a[i] = load8((const T*)(shared_base(pa + (slice * VA + i) * sa) + oa)); };
-        const auto load_b = [&](int64_t slice, int i) { c[i] = ldg((const u32x2*)(shared_base(pc + (slice * VB + i) * sc) + oc)); };
-        const auto load_e = [&](int64_t slice, int i) { e[i] = ldg((const u32x2*)(shared_base(pe + (slice * (KS / 32) + i) * pitch) + oe)); };
-        // the scales of a block of 32 tokens follow its last codes
-        constexpr int PER_E = 32 / BR;
-#pragma unroll
-        for (int i = 0; i < VA; ++i) load_a(0, i);
-#pragma unroll
-        for (int i = 0; i < VB; ++i) load_b(0, i);
-#pragma unroll
-        for (int i = 0; i < KS / 32; ++i) load_e(0, i);
-        const auto stage = [&](int buf, int64_t next, int i0a, int i1a, int i0b, int i1b) {
+        const auto load_a = [&](int i) {
+            using M = __attribute__((address_space(1))) const typename Vec8<T>::Mem;
+            a[i] = *(M*)(base(na + i * sa) + oa);
+        };
+        const auto load_b = [&](int i) {
+            using M = __attribute__((address_space(1))) const u32x2;
+            c[i] = *(M*)(base(nc + i * sc) + oc);
+            // the scales of a block of 32 tokens follow its last codes
+            constexpr int PER_E = 32 / BR;
+            if ((i + 1) % PER_E == 0) e[i / PER_E] = *(M*)(base(ne + i / PER_E * pitch) + oe);
+        };
+        // the last slice is loaded again rather than none
+        const auto advance = [&](bool more) {
+            na += more ? VA * sa : 0;
+            nc += more ? VB * sc : 0;
+            ne += more ? KS / 32 * pitch : 0;
+        };
+        // a part of the loaded slice to LDS, and of the next one on its way
+        const auto stage = [&](int buf, int i0a, int i1a, int i0b, int i1b) {
 #pragma unroll
             for (int i = i0a; i < i1a; ++i) {
                 store_a(buf, i);
-                load_a(next, i);
+                load_a(i);
             }
 #pragma unroll
             for (int i = i0b; i < i1b; ++i) {
                 store_b(buf, i);
-                load_b(next, i);
-                if ((i + 1) % PER_E == 0) load_e(next, i / PER_E);
+                load_b(i);
             }
         };
-        stage(0, min<int64_t>(1, fast - 1), 0, VA, 0, VB);
-        __syncthreads();
-        Frags f[2];
-        read_frags(f[0], 0, 0);
-        for (int64_t s = 0; s < fast; ++s) {
-            const int buf = (int)s & 1;
-            const int64_t next = min(s + 2, fast - 1);
 #pragma unroll
-            for (int ks = 0; ks < STEPS; ++ks) {
-                // The next slice is whole in LDS before the last step, and this slice's last
+        for (int i = 0; i < VA; ++i) load_a(i);
+#pragma unroll
+        for (int i = 0; i < VB; ++i) load_b(i);
+        advance(1 < fast);
+        stage(0, 0, VA, 0, VB);
+        __syncthreads();
+        read_unit(0, 0);
+        const auto slice = [&](int buf, bool more) {
+            advance(more);
+#pragma unroll
+            for (int u = 0; u < S::UNITS; ++u) {
+                // The next slice is whole in LDS before the last unit, and this slice's last
                 // operands are in registers: the one barrier of a slice, with products to
                 // follow it while the next operands are read.
-                if (ks == STEPS - 1) __syncthreads();
-                read_frags(f[(ks + 1) & 1], ks == STEPS - 1 ? buf ^ 1 : buf, (ks + 1) % STEPS);
-                products(f[ks & 1]);
-                // a part of the next slice to the other stage, and of the one after it on its way
-                constexpr int P = STEPS - 1;
-                if (ks < P) stage(buf ^ 1, next, ks * VA / P, (ks + 1) * VA / P, ks * VB / P, (ks + 1) * VB / P);
+                if (u == S::UNITS - 1) __syncthreads();
+                read_unit(u == S::UNITS - 1 ? buf ^ 1 : buf, (u + 1) % S::UNITS);
+                products(u);
+                constexpr int P = S::UNITS - 1;
+                if (u < P) stage(buf ^ 1, u * VA / P, (u + 1) * VA / P, u * VB / P, (u + 1) * VB / P);
+                // operand reads and the staging's arithmetic in the shadow of the products
+#pragma unroll
+                for (int q = 0; q < TM * TN; ++q) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);       // matrix core
+                    __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);       // LDS reads
+                    __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);       // vector
+                }
                 // without this the loads gather at the slice's end and are waited for at once
                 __builtin_amdgcn_sched_barrier(0);
             }
+        };
+        // two slices a turn, so that the stage is a constant of every address
+        for (int64_t s = 0; s < fast; s += 2) {
+            slice(0, s + 2 < fast);
+            if (s + 1 < fast) slice(1, s + 3 < fast);
         }
         __syncthreads();
     }
@@ -246,7 +272,8 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
             a[i] = load8_n((const T*)w.dy + row * w.lddy + m0 + acol, row < r1 ? n : 0);
         }
 #pragma unroll
-        for (int i = 0; i < KS / 32; ++i) e[i] = k + 32 * i < r1 ? ldg((const u32x2*)(w.scales + (k / 32 + i) * pitch + bn)) : u32x2{0, 0};
+        for (int i = 0; i < KS / 32; ++i)
+            e[i] = k + 32 * i < r1 ? ldg((const u32x2*)(w.scales + (k / 32 + i) * pitch + bn)) : u32x2{0, 0};
 #pragma unroll
         for (int i = 0; i < VB; ++i) {
             const int64_t row = k + brow + i * BR;
@@ -260,10 +287,9 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
         for (int i = 0; i < VB; ++i) store_b(0, i);
         __syncthreads();
 #pragma unroll
-        for (int ks = 0; ks < STEPS; ++ks) {
-            Frags f;
-            read_frags(f, 0, ks);
-            products(f);
+        for (int u = 0; u < S::UNITS; ++u) {
+            read_unit(0, u);
+            products(u);
         }
     }
 
@@ -331,7 +357,7 @@ template <class T>
 hipError_t wgrad_of(const WGrad& w, const WPlan& p, hipStream_t stream) {
     // three pieces of a 64-token slice would not fit twice into LDS
     constexpr int KS = Pieces<T>::N == 1 ? 64 : 32;
-    return p.large ? wgrad_launch<T, 2, 4, 4, 2, KS>(w, p, stream) : wgrad_launch<T, 2, 2, 2, 2, 32>(w, p, stream);
+    return p.large ? wgrad_launch<T, 2, 4, 4, 2, KS>(w, p, stream) : wgrad_launch<T, 2, 4, 2, 1, KS>(w, p, stream);
 }
 
 }  // namespace
