@@ -290,9 +290,46 @@ __global__ __launch_bounds__(256) void policy_join_kernel(Policy p, Pieces q, fl
     }
 }
 
-// A piece of a row's gradient.
-template <class T>
+// The loss and the log-probabilities of a few rows, by one workgroup of 256: sixteen lanes a
+// row, each row's terms in order.
+__device__ void few_rows_loss(const Policy& p, const Pieces& q) {
+    __shared__ float part[16];
+    const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+    float sum = 0.f;
+    for (int64_t t = group; t < p.rows; t += 16) {
+        float logp = 0.f;
+        if (target_of(p, t) >= 0) {
+            const float* st = q.stat + 2 * t * q.pieces;
+            float ref = NEG_INF;
+            for (int64_t i = lane; i < q.pieces; i += 16) ref = fmaxf(ref, ldg(st + 2 * i));
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o));
+            const float base = base_of(ref);
+            float s = 0.f;
+            for (int64_t i = lane; i < q.pieces; i += 16) s += rebase(ldg(st + 2 * i + 1), ldg(st + 2 * i), base);
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+            logp = log_prob(ldg(q.zy + t), base, s);
+            sum += row_term(p, t, logp).loss;
+        }
+        if (lane == 0 && p.logp) stg(p.logp + t, logp);
+    }
+    if (lane == 0) part[group] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < 16; ++i) sum += part[i];
+        stg(p.loss, sum);
+    }
+}
+
+// A piece of a row's gradient; with LOSS, one more workgroup writes the loss and the
+// log-probabilities beside them.
+template <class T, bool LOSS>
 __global__ __launch_bounds__(256) void policy_grad_kernel(Policy p, Pieces q) {
+    if (LOSS && blockIdx.x == gridDim.x - 1) {
+        few_rows_loss(p, q);
+        return;
+    }
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x / q.pieces, piece = blockIdx.x - t * q.pieces;
     const T* z = (const T*)p.logits + t * p.ldz;
@@ -339,7 +376,12 @@ __global__ __launch_bounds__(1024) void loss_sum_kernel(const float* __restrict_
     }
 }
 
-constexpr int64_t SPLIT_ROWS = 64;           // fewer rows are split
+// Up to SPLIT_ROWS rows are split.  Measured (split launches against the row kernel and the
+// loss's): 8 x 32768 bf16 7.8 us against 11.4, 8 x 40961 fp32 7.9 against 12.2, 63 x 65536
+// bf16 11.7 against 14.6, 48 x 131072 bf16 11.2 against 19.9.  Shorter rows are a few
+// microseconds either way and take the row kernel; so do the log-probabilities alone up to
+// 32768 logits, one launch instead of two.
+constexpr int64_t SPLIT_ROWS = 64;
 constexpr int64_t SPLIT_GROUPS = 1024;       // workgroups of a split launch, about
 
 struct PolicyPlan {
@@ -347,11 +389,11 @@ struct PolicyPlan {
     int64_t pieces, vecs;
     size_t off_stat, off_zy, total;          // the rows' terms come first
 };
-PolicyPlan policy_plan(shampoo4_dtype dtype, int64_t rows, int64_t vocab) {
+PolicyPlan policy_plan(shampoo4_dtype dtype, int64_t rows, int64_t vocab, bool train) {
     PolicyPlan q{};
     const int64_t nvec = vocab >> 3;
     const int64_t most = 1024 * (dtype == SHAMPOO4_F32 ? 8 : 16);    // vectors a workgroup holds
-    q.split = nvec > most || (rows < SPLIT_ROWS && nvec > 1024);
+    q.split = nvec > most || (rows <= SPLIT_ROWS && nvec > (train ? 1024 : 4096));
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     q.off_stat = up((size_t)rows * 4);
     q.total = q.off_stat;
@@ -371,17 +413,22 @@ void row_kernel(const Policy& p, float* terms, hipStream_t stream) {
     S4_LAUNCH((policy_row_kernel<T, THREADS, NV>), dim3((uint32_t)p.rows), dim3(THREADS), 0, stream, p, terms);
 }
 
+// Returns whether the rows' terms are left to sum.
 template <class T>
-void policy_of(const Policy& p, const PolicyPlan& plan, char* ws, hipStream_t stream) {
+bool policy_of(const Policy& p, const PolicyPlan& plan, char* ws, hipStream_t stream) {
     float* terms = (float*)ws;
     constexpr int W = sizeof(T) == 4 ? 1 : 2;                // vectors per 64 data registers: 8 or 16
     const int64_t nvec = p.vocab >> 3;
     if (plan.split) {
         const Pieces q{(float*)(ws + plan.off_stat), (float*)(ws + plan.off_zy), plan.pieces, plan.vecs};
-        const dim3 grid((uint32_t)(p.rows * plan.pieces));
-        S4_LAUNCH(policy_part_kernel<T>, grid, dim3(256), 0, stream, p, q);
+        const uint32_t n = (uint32_t)(p.rows * plan.pieces);
+        S4_LAUNCH(policy_part_kernel<T>, dim3(n), dim3(256), 0, stream, p, q);
+        if (p.train && p.rows <= SPLIT_ROWS) {
+            S4_LAUNCH((policy_grad_kernel<T, true>), dim3(p.dlogits ? n + 1 : 1), dim3(256), 0, stream, p, q);
+            return false;
+        }
         S4_LAUNCH(policy_join_kernel, dim3((uint32_t)((p.rows + 3) / 4)), dim3(256), 0, stream, p, q, terms);
-        if (p.dlogits) S4_LAUNCH(policy_grad_kernel<T>, grid, dim3(256), 0, stream, p, q);
+        if (p.dlogits) S4_LAUNCH((policy_grad_kernel<T, false>), dim3(n), dim3(256), 0, stream, p, q);
     } else if (nvec <= 256 * 2 * W) {
         row_kernel<T, 256, 2 * W>(p, terms, stream);
     } else if (nvec <= 256 * 8 * W) {
@@ -391,25 +438,27 @@ void policy_of(const Policy& p, const PolicyPlan& plan, char* ws, hipStream_t st
     } else {
         row_kernel<T, 1024, 8 * W>(p, terms, stream);
     }
+    return p.train;
 }
 
 }  // namespace
 
 size_t policy_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab) {
-    return policy_plan(dtype, rows, vocab).total;
+    return policy_plan(dtype, rows, vocab, true).total;
 }
 
 hipError_t launch_policy(shampoo4_dtype dtype, const Policy& p, void* workspace, hipStream_t stream) {
-    const PolicyPlan plan = policy_plan(dtype, p.rows, p.vocab);
+    const PolicyPlan plan = policy_plan(dtype, p.rows, p.vocab, p.train != 0);
     if (p.rows == 0 && !p.train) return hipSuccess;
+    bool sum = p.train;
     if (p.rows > 0) {
         switch (dtype) {
-            case SHAMPOO4_BF16: policy_of<__bf16>(p, plan, (char*)workspace, stream); break;
-            case SHAMPOO4_F16: policy_of<_Float16>(p, plan, (char*)workspace, stream); break;
-            default: policy_of<float>(p, plan, (char*)workspace, stream);
+            case SHAMPOO4_BF16: sum = policy_of<__bf16>(p, plan, (char*)workspace, stream); break;
+            case SHAMPOO4_F16: sum = policy_of<_Float16>(p, plan, (char*)workspace, stream); break;
+            default: sum = policy_of<float>(p, plan, (char*)workspace, stream);
         }
     }
-    if (p.train)
+    if (sum)
         S4_LAUNCH(loss_sum_kernel, dim3(1), dim3(1024), 0, stream, (const float*)workspace, p.rows, p.loss);
     return hipGetLastError();
 }

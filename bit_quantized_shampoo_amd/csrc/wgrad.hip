@@ -312,15 +312,27 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
             }
 }
 
-// G = alpha sum_s parts[s] + beta G, the parts in order.
+// G = alpha sum_s parts[s] + beta G, the parts in order; V consecutive elements a thread
+// (V = 4 where rows are multiples of four long).
+template <int V>
 __global__ __launch_bounds__(256) void wgrad_sum_kernel(WGrad w, int splits) {
+    typedef float Vec __attribute__((ext_vector_type(V)));
+    typedef Vec Mem __attribute__((aligned(4)));
+    using G = __attribute__((address_space(1))) Mem;
     const int64_t n = w.n * w.cols;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        float s = 0.f;
-        for (int k = 0; k < splits; ++k) s += ldg(w.parts + k * n + i);
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * V; i < n; i += gridDim.x * 256ll * V) {
+        Vec s = *(G*)(w.parts + i);
+        int k = 1;
+        for (; k + 3 <= splits; k += 3) {
+            const Vec a = *(G*)(w.parts + k * n + i), b = *(G*)(w.parts + (k + 1) * n + i), c = *(G*)(w.parts + (k + 2) * n + i);
+            s = ((s + a) + b) + c;
+        }
+        for (; k < splits; ++k) s += *(G*)(w.parts + k * n + i);
         const int64_t r = i / w.cols;
-        float* p = w.g + r * w.ldg + (i - r * w.cols);
-        stg(p, w.beta != 0.f ? fmaf(w.alpha, s, w.beta * ldg(p)) : w.alpha * s);
+        G* p = (G*)(w.g + r * w.ldg + (i - r * w.cols));
+        s *= w.alpha;
+        if (w.beta != 0.f) s += w.beta * *p;
+        *p = s;
     }
 }
 
@@ -329,17 +341,37 @@ struct WPlan {
     int64_t tiles_m, tiles_n, rows_per;
     int splits;
 };
+// Tile and row ranges by an estimate of the time.  A round of workgroups (one a CU) takes
+// 28 ns a token on 256 x 256 tiles and 11 ns on 128 x 128 ones (bf16, measured where the
+// rounds are full: 16384 x 4096 x 4096 in 463 us against 663 us in four times the tiles).
+// Row ranges beyond one fill the GPU when the output alone cannot, at the cost of writing
+// and reading their partial sums (5 bytes a ns, and 2000 ns for the launch that joins them):
+// 16384 x 1024 x 4096 takes 142 us in four ranges of 64 large tiles, 182 us in 256 small
+// tiles and 351 us in 64 large ones; 2048 x 2048 x 2048 28 us in 256 small tiles, 44 us in
+// four ranges of 64 large ones.  A range has at least 128 tokens.
 WPlan wgrad_plan(int64_t rows, int64_t n, int64_t cols) {
-    WPlan p;
-    p.large = ((n + 255) / 256) * ((cols + 255) / 256) >= 128;
-    const int64_t tile = p.large ? 256 : 128;
-    p.tiles_m = (n + tile - 1) / tile;
-    p.tiles_n = (cols + tile - 1) / tile;
-    const int64_t tiles = p.tiles_m * p.tiles_n;
-    const int64_t s = p.large ? 1 : std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), rows / 256));
-    p.rows_per = ((rows + s - 1) / s + 63) / 64 * 64;
-    p.splits = rows > 0 ? (int)((rows + p.rows_per - 1) / p.rows_per) : 1;
-    return p;
+    WPlan best{};
+    double best_ns = 0;
+    for (int k = 0; k < 2; ++k) {
+        WPlan p;
+        p.large = k == 1;
+        const int64_t tile = p.large ? 256 : 128;
+        p.tiles_m = (n + tile - 1) / tile;
+        p.tiles_n = (cols + tile - 1) / tile;
+        const int64_t tiles = p.tiles_m * p.tiles_n;
+        for (int64_t s = 1; s <= 16 && (s == 1 || (rows / s >= 128 && tiles * s <= 512)); ++s) {
+            p.rows_per = ((rows + s - 1) / s + 63) / 64 * 64;
+            p.splits = rows > 0 ? (int)((rows + p.rows_per - 1) / p.rows_per) : 1;
+            if (p.splits != s) continue;
+            double ns = (double)((tiles * s + 255) / 256) * (double)p.rows_per * (p.large ? 28. : 11.);
+            if (s > 1) ns += 2000. + (2. * s + 1) * (double)(n * cols) * 4 / 5e3;
+            if (best.splits == 0 || ns < best_ns) {
+                best = p;
+                best_ns = ns;
+            }
+        }
+    }
+    return best;
 }
 
 template <class T, int WM, int WN, int TM, int TN, int KS>
@@ -379,8 +411,13 @@ hipError_t launch_wgrad(shampoo4_dtype dtype, const WGrad& w, hipStream_t stream
     }
     if (e != hipSuccess) return e;
     if (part) {
-        const dim3 sg((uint32_t)std::min<int64_t>((w.n * w.cols + 255) / 256, 4096));
-        S4_LAUNCH(wgrad_sum_kernel, sg, dim3(256), 0, stream, w, p.splits);
+        const bool four = w.cols % 4 == 0;
+        const int64_t threads = w.n * w.cols / (four ? 4 : 1);
+        const dim3 sg((uint32_t)std::min<int64_t>((threads + 255) / 256, 4096));
+        if (four)
+            S4_LAUNCH(wgrad_sum_kernel<4>, sg, dim3(256), 0, stream, w, p.splits);
+        else
+            S4_LAUNCH(wgrad_sum_kernel<1>, sg, dim3(256), 0, stream, w, p.splits);
     }
     return hipGetLastError();
 }
