@@ -17,8 +17,11 @@ namespace {
 struct Tile {
     int64_t row0;             // this lane's first row
     int64_t col0;             // this lane's first column
+    int64_t rows, cols;
     int nrow, ncol;           // valid rows and columns of the lane, 0..8
     int64_t block;            // block of 32 rows
+    bool full;                // the wave's rows and columns all exist
+    bool vectors;             // no lane's columns end inside its eight
 };
 
 __device__ __forceinline__ Tile lane_tile(int64_t rows, int64_t cols, int64_t ntiles, bool& live) {
@@ -27,45 +30,50 @@ __device__ __forceinline__ Tile lane_tile(int64_t rows, int64_t cols, int64_t nt
     live = tile < ntiles;
     const uint32_t ncb = (uint32_t)((cols + ACT8_COLS - 1) / ACT8_COLS);
     Tile t;
+    t.rows = rows;
+    t.cols = cols;
     t.block = tile / ncb;
     t.row0 = t.block * 32 + (lane >> 4) * 8;
     t.col0 = (int64_t)(tile % ncb) * ACT8_COLS + (lane & 15) * 8;
     t.nrow = (int)max((int64_t)0, min((int64_t)8, rows - t.row0));
     t.ncol = (int)max((int64_t)0, min((int64_t)8, cols - t.col0));
+    t.full = __all(t.nrow == 8 && t.ncol == 8);
+    t.vectors = cols >= 8 && __all(t.ncol == 8 || t.ncol == 0);
     return t;
 }
 
-// The wave's tile is whole: no masks.
-__device__ __forceinline__ bool whole(const Tile& t) { return __all(t.nrow == 8 && t.ncol == 8); }
-
+// The lane's eight rows of eight columns, zeros outside the matrix.  No load is under a
+// lane's own condition: rows and columns are clamped into the matrix, and masked.
 template <class T>
-__device__ __forceinline__ void load_tile(typename Vec8<T>::Raw (&r)[8], const T* p, int64_t ld, const Tile& t,
-                                          bool full) {
-    p += t.row0 * ld + t.col0;
-    if (full) {
+__device__ __forceinline__ void load_tile(typename Vec8<T>::Raw (&r)[8], const T* p, int64_t ld, const Tile& t) {
+    if (t.full) {
+        p += t.row0 * ld + t.col0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[i] = load8(p + i * ld);
+    } else if (t.vectors) {
+        p += t.ncol ? t.col0 : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = load8(p + min(t.row0 + i, t.rows - 1) * ld);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] &= i < t.nrow && t.ncol ? 0xffffffffu : 0u;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = load8_n(p + i * ld, i < t.nrow ? t.ncol : 0);
+        for (int i = 0; i < 8; ++i) r[i] = load8_clamped(p + min(t.row0 + i, t.rows - 1) * ld, t.col0, t.cols);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] &= i < t.nrow ? 0xffffffffu : 0u;
     }
 }
 
 template <class T>
-__device__ __forceinline__ void store_tile(const typename Vec8<T>::Raw (&r)[8], T* p, int64_t ld, const Tile& t,
-                                           bool full) {
+__device__ __forceinline__ void store_tile(const typename Vec8<T>::Raw (&r)[8], T* p, int64_t ld, const Tile& t) {
     p += t.row0 * ld + t.col0;
-    if (full) {
+    if (t.full) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) store8(p + i * ld, r[i]);
     } else {
-        for (int i = 0; i < t.nrow; ++i) {
-            typename Vec8<T>::Raw v = r[0];
 #pragma unroll
-            for (int j = 1; j < 8; ++j)
-                if (i == j) v = r[j];
-            store8_n(p + i * ld, v, t.ncol);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (i < t.nrow) store8_n(p + i * ld, r[i], t.ncol);
     }
 }
 
@@ -91,17 +99,22 @@ __device__ __forceinline__ void exponents(const typename Vec8<T>::Raw (&r)[8], u
 // Codes and exponents of a loaded tile.  Every lane inside the padded columns writes
 // (padding rows and columns hold zeros); the first row group writes the exponents.
 template <class T>
-__device__ __forceinline__ void encode_tile(const typename Vec8<T>::Raw (&r)[8], Act8Ptr out, int64_t pitch,
+__device__ __forceinline__ void encode_tile(typename Vec8<T>::Raw (&r)[8], Act8Ptr out, int64_t pitch,
                                             const Tile& t) {
     uint32_t e[8];
     exponents<T>(r, e);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) unpack_again(r[i]);
     if (t.col0 >= pitch) return;
     Act8Block blk;
 #pragma unroll
     for (int j = 0; j < 8; ++j) blk.set(j, e[j]);
     int8_t* c = out.codes + t.row0 * pitch + t.col0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) stg((u32x2*)(c + i * pitch), blk.codes(Vec8<T>::get(r[i])));
+    for (int i = 0; i < 8; ++i) {
+        stg((u32x2*)(c + i * pitch), blk.codes(Vec8<T>::get(r[i])));
+        unpack_again(r[i]);
+    }
     if ((threadIdx.x & 63) < 16) {
         u32x2 p;
         p[0] = e[0] | e[1] << 8 | e[2] << 16 | e[3] << 24;
@@ -121,7 +134,7 @@ __global__ __launch_bounds__(256) void act8_store_kernel(const T* __restrict__ x
     const Tile t = lane_tile(rows, cols, ntiles, live);
     if (!live) return;
     typename Vec8<T>::Raw r[8];
-    load_tile(r, x, ldx, t, whole(t));
+    load_tile(r, x, ldx, t);
     encode_tile<T>(r, out, act8_pitch(cols), t);
 }
 
@@ -153,16 +166,17 @@ __global__ __launch_bounds__(256) void act8_load_kernel(Act8Ptr in, T* __restric
     typename Vec8<T>::Raw r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = Vec8<T>::put(saturate<T>(act8_values(q[i], s)));
-    store_tile(r, x, ldx, t, whole(t));
+    store_tile(r, x, ldx, t);
 }
 
 // a(x) and a'(x) = sg + x sg (1 - sg) z'(x) with sg = 1 / (1 + exp(-z)): z = x (SiLU) or
 // 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU, tanh form).  No difference of near values, so
-// small and large arguments keep their relative precision.
+// small and large arguments keep their relative precision.  The hardware exp2 and reciprocal
+// (1 ulp each) do: the argument's own rounding, |z| 2^-24 of the result, is larger.
 template <int KIND>
 __device__ __forceinline__ float act_sigmoid(float x) {
     const float z = KIND == SHAMPOO4_ACT_SILU ? x : 1.5957691216f * fmaf(0.044715f * x * x, x, x);
-    return 1.f / (1.f + expf(-z));
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950409f * z));
 }
 template <int KIND>
 __device__ __forceinline__ float act_derivative(float x, float sg) {
@@ -175,11 +189,10 @@ __global__ __launch_bounds__(256) void act_forward_kernel(ActForward a, int64_t 
     bool live;
     const Tile t = lane_tile(a.rows, a.cols, ntiles, live);
     if (!live) return;
-    const bool full = whole(t);
     const int64_t pitch = act8_pitch(a.cols);
     typename Vec8<T>::Raw g[8], u[8];
-    load_tile(g, (const T*)a.gate, a.ldgate, t, full);
-    if constexpr (GATED) load_tile(u, (const T*)a.up, a.ldup, t, full);
+    load_tile(g, (const T*)a.gate, a.ldgate, t);
+    if constexpr (GATED) load_tile(u, (const T*)a.up, a.ldup, t);
     if (a.gate8.codes) encode_tile<T>(g, a.gate8, pitch, t);
     if constexpr (GATED)
         if (a.up8.codes) encode_tile<T>(u, a.up8, pitch, t);
@@ -191,8 +204,9 @@ __global__ __launch_bounds__(256) void act_forward_kernel(ActForward a, int64_t 
         for (int j = 0; j < 8; ++j) h[j] = x[j] * act_sigmoid<KIND>(x[j]);
         if constexpr (GATED) h *= Vec8<T>::get(u[i]);
         g[i] = Vec8<T>::put(h);
+        __builtin_amdgcn_sched_barrier(0);     // one row's values at a time in registers
     }
-    store_tile(g, (T*)a.h, a.ldh, t, full);
+    store_tile(g, (T*)a.h, a.ldh, t);
     if (a.h8.codes) encode_tile<T>(g, a.h8, pitch, t);
 }
 
@@ -202,7 +216,6 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int64_
     const Tile t = lane_tile(a.rows, a.cols, ntiles, live);
     const int64_t pitch = act8_pitch(a.cols);
     if (!live || t.col0 >= pitch) return;
-    const bool full = whole(t);
     const int64_t at = t.row0 * pitch + t.col0;
     u32x2 cg[8], cu[8];
 #pragma unroll
@@ -210,28 +223,34 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int64_
         cg[i] = ldg_u2(a.gate8.codes + at + i * pitch);
         if constexpr (GATED) cu[i] = ldg_u2(a.up8.codes + at + i * pitch);
     }
-    typename Vec8<T>::Raw d[8], du[8];
-    load_tile(d, (const T*)a.dh, a.lddh, t, full);
+    typename Vec8<T>::Raw d[8];
+    load_tile(d, (const T*)a.dh, a.lddh, t);
     const floatx8 sg = load_scales(a.gate8.scales, pitch, t);
     floatx8 su;
     if constexpr (GATED) su = load_scales(a.up8.scales, pitch, t);
+    T* pg = (T*)a.dgate + t.row0 * a.lddgate + t.col0;
+    T* pu = (T*)a.dup + t.row0 * a.lddup + t.col0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const floatx8 x = act8_values(cg[i], sg);
-        floatx8 dx = Vec8<T>::get(d[i]);
-        floatx8 s;
+        const floatx8 dx = Vec8<T>::get(d[i]);
+        floatx8 s, dg, du;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] = act_sigmoid<KIND>(x[j]);
-        if constexpr (GATED) {
-            du[i] = Vec8<T>::put(dx * x * s);
-            dx *= act8_values(cu[i], su);
+        for (int j = 0; j < 8; ++j) {
+            s[j] = act_sigmoid<KIND>(x[j]);
+            dg[j] = dx[j] * act_derivative<KIND>(x[j], s[j]);
+            du[j] = dx[j] * (x[j] * s[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dx[j] *= act_derivative<KIND>(x[j], s[j]);
-        d[i] = Vec8<T>::put(dx);
+        if constexpr (GATED) dg *= act8_values(cu[i], su);
+        if (t.full) {
+            store8(pg + i * a.lddgate, Vec8<T>::put(dg));
+            if constexpr (GATED) store8(pu + i * a.lddup, Vec8<T>::put(du));
+        } else if (i < t.nrow) {
+            store8_n(pg + i * a.lddgate, Vec8<T>::put(dg), t.ncol);
+            if constexpr (GATED) store8_n(pu + i * a.lddup, Vec8<T>::put(du), t.ncol);
+        }
+        __builtin_amdgcn_sched_barrier(0);     // one row's values at a time in registers
     }
-    store_tile(d, (T*)a.dgate, a.lddgate, t, full);
-    if constexpr (GATED) store_tile(du, (T*)a.dup, a.lddup, t, full);
 }
 
 dim3 wave_grid(int64_t ntiles) { return dim3((uint32_t)((ntiles + 3) / 4)); }

@@ -97,15 +97,18 @@ __device__ void fill_zeros(const Fill& f, int64_t blk, int64_t nblk) {
     }
 }
 
-// Lanes of this wave with the same digit as this one (live lanes only).
+// Lanes of this wave with the same digit as this one (live lanes only).  A lane's bit as a
+// mask x of ones or zeros keeps the lanes whose bit agrees: m & ~(ballot ^ x).
 __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool live, int bits) {
-    uint64_t m = __ballot(live);
+    const uint64_t all = __ballot(live);
+    uint32_t lo = (uint32_t)all, hi = (uint32_t)(all >> 32);
     for (int b = 0; b < bits; ++b) {
-        const bool one = (digit >> b) & 1;
-        const uint64_t w = __ballot(one && live);
-        m &= one ? w : ~w;
+        const int x = (int)(digit << (31 - b)) >> 31;
+        const uint64_t w = __ballot(x < 0);
+        lo &= ~((uint32_t)w ^ (uint32_t)x);
+        hi &= ~((uint32_t)(w >> 32) ^ (uint32_t)x);
     }
-    return m;
+    return (uint64_t)hi << 32 | lo;
 }
 
 // Stable ranks of a workgroup's items by digit.  Wave w's item of round r is number
@@ -114,19 +117,18 @@ __device__ __forceinline__ uint64_t same_digit(uint32_t digit, bool live, int bi
 template <int ROUNDS>
 __device__ __forceinline__ void wave_ranks(const uint32_t (&digit)[ROUNDS], const bool (&live)[ROUNDS], int bits,
                                            uint32_t* cnt, uint32_t (&rank)[ROUNDS], int rounds) {
-    const int lane = threadIdx.x & 63;
-    const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r) {
         if (r < rounds) {
             const uint64_t m = same_digit(digit[r], live[r], bits);
             uint32_t old = 0;
             if (live[r]) old = cnt[digit[r]];
-            rank[r] = old + __popcll(m & below);
+            const uint32_t first = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+            rank[r] = old + first;
             // the next round reads what this one's first lane writes: LDS accesses of a wave
             // execute in order, and the fences keep the compiler to it
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (live[r] && (m & below) == 0) cnt[digit[r]] = old + __popcll(m);
+            if (live[r] && first == 0) cnt[digit[r]] = old + __popcll(m);
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         }
     }
@@ -301,59 +303,59 @@ struct RunSum {
     const uint32_t* key;      // sorted ids
     const uint32_t* pos;      // their positions
     float* g;
-    float* first;             // [chunks][dim] run that began in an earlier chunk
-    float* last;              // [chunks][dim] run that begins here and goes on
-    int64_t tokens, dim, lddout, ldg;
+    float* first;             // [chunks][pitch] run that began in an earlier chunk
+    float* last;              // [chunks][pitch] run that begins here and goes on
+    int64_t tokens, dim, pitch, lddout, ldg;
     uint32_t vocab, chunks, col_tiles;
     float scale;
     int accumulate;
 };
 
-// Eight columns of one row of G.
-__device__ __forceinline__ void put_row(const RunSum& s, uint32_t key, int64_t c, int n, floatx8 acc) {
-    float* p = s.g + (int64_t)key * s.ldg + c;
-    floatx8 v = acc * s.scale;
-    if (s.accumulate) v += Vec8<float>::get(load8_n(p, n));
-    store8_n(p, Vec8<float>::put(v), n);
+// A lane's eight columns of a row: whole vectors where no lane of the wave has its columns end
+// inside them, else element by element; clamped into the row, so that no load is under a
+// lane's own condition.
+struct Cols {
+    int64_t c, dim;
+    int n;                    // valid columns, 0..8
+    bool vectors;
+};
+__device__ __forceinline__ Cols lane_cols(int64_t tile, int64_t dim) {
+    Cols k;
+    k.c = tile * COLS + (threadIdx.x & 63) * 8;
+    k.dim = dim;
+    k.n = (int)max((int64_t)0, min((int64_t)8, dim - k.c));
+    k.vectors = dim >= 8 && __all(k.n == 8 || k.n == 0);
+    return k;
+}
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::Raw load_cols(const T* row, const Cols& k) {
+    return k.vectors ? load8(row + (k.n ? k.c : 0)) : load8_clamped(row, k.c, k.dim);
 }
 
-template <class T>
-__global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
-    const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
-    const uint32_t chunk = wave / s.col_tiles;
-    if (chunk >= s.chunks) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t c = (int64_t)(wave - chunk * s.col_tiles) * COLS + lane * 8;
-    const int n = (int)max((int64_t)0, min((int64_t)8, s.dim - c));
-    const int64_t i0 = (int64_t)chunk * CHUNK;
-    const int count = (int)min((int64_t)CHUNK, s.tokens - i0);
-    // lane i < CHUNK holds position i0 + i; lanes CHUNK and CHUNK + 1 the keys on either side
-    uint32_t k = 0xffffffffu, p = 0;
-    if (lane < count) {
-        k = ldg(s.key + i0 + lane);
-        p = ldg(s.pos + i0 + lane);
-    } else if (lane == CHUNK && i0 > 0) {
-        k = ldg(s.key + i0 - 1);
-    } else if (lane == CHUNK + 1 && i0 + CHUNK < s.tokens) {
-        k = ldg(s.key + i0 + CHUNK);
-    }
+// Sums of a chunk's runs, BATCH positions in flight at a time; with ACC the rows of G that a
+// run is added to are loaded beside them, for every position (those of one run are one row).
+template <class T, bool ACC, int BATCH>
+__device__ __forceinline__ void run_sums(const RunSum& s, const Cols& cols, uint32_t chunk, uint32_t k, uint32_t p) {
     const uint32_t prev = (uint32_t)__builtin_amdgcn_readlane((int)k, CHUNK);
     const uint32_t next = (uint32_t)__builtin_amdgcn_readlane((int)k, CHUNK + 1);
-    const T* dout = (const T*)s.dout + c;
     floatx8 acc = {};
     bool begun_before = (uint32_t)__builtin_amdgcn_readlane((int)k, 0) == prev;
 #pragma unroll
-    for (int b = 0; b < CHUNK; b += 8) {
-        typename Vec8<T>::Raw r[8];
+    for (int b = 0; b < CHUNK; b += BATCH) {
+        typename Vec8<T>::Raw r[BATCH];
+        typename Vec8<float>::Raw g[ACC ? BATCH : 1];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            r[i] = typename Vec8<T>::Raw{};
-            const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
+        for (int i = 0; i < BATCH; ++i) {
+            // positions past the end and tokens without a row load a row that exists
             const uint32_t row = (uint32_t)__builtin_amdgcn_readlane((int)p, b + i);
-            if (key < s.vocab) r[i] = load8_n(dout + (int64_t)row * s.lddout, n);
+            r[i] = load_cols((const T*)s.dout + (int64_t)row * s.lddout, cols);
+            if constexpr (ACC) {
+                const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
+                g[i] = load_cols((const float*)s.g + (int64_t)(key < s.vocab ? key : 0) * s.ldg, cols);
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
             if (key >= s.vocab) return;        // tokens without a row come last
             const uint32_t after = b + i + 1 < CHUNK ? (uint32_t)__builtin_amdgcn_readlane((int)k, (b + i + 1) % 64) : next;
@@ -361,19 +363,39 @@ __global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
             const bool at_end = b + i + 1 == CHUNK;
             if (key != after || at_end) {
                 const bool goes_on = at_end && key == after;
-                if (n > 0) {
-                    if (begun_before)
-                        store8_n(s.first + (int64_t)chunk * s.dim + c, Vec8<float>::put(acc), n);
-                    else if (goes_on)
-                        store8_n(s.last + (int64_t)chunk * s.dim + c, Vec8<float>::put(acc), n);
-                    else
-                        put_row(s, key, c, n, acc);
+                if (begun_before || goes_on) {
+                    float* part = (begun_before ? s.first : s.last) + (int64_t)chunk * s.pitch + cols.c;
+                    if (cols.n > 0) store8(part, Vec8<float>::put(acc));
+                } else {
+                    floatx8 v = acc * s.scale;
+                    if constexpr (ACC) v += Vec8<float>::get(g[i]);
+                    store8_n(s.g + (int64_t)key * s.ldg + cols.c, Vec8<float>::put(v), cols.n);
                 }
                 acc = floatx8{};
                 begun_before = false;
             }
         }
     }
+}
+
+template <class T, bool ACC>
+__global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
+    const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const uint32_t chunk = wave / s.col_tiles;
+    if (chunk >= s.chunks) return;
+    const int lane = threadIdx.x & 63;
+    const Cols cols = lane_cols(wave - chunk * s.col_tiles, s.dim);
+    const int64_t i0 = (int64_t)chunk * CHUNK;
+    const int count = (int)min((int64_t)CHUNK, s.tokens - i0);
+    // lane i < CHUNK holds position i0 + i; lanes CHUNK and CHUNK + 1 the keys on either side
+    uint32_t k = 0xffffffffu, p = 0;
+    const int64_t at = lane < CHUNK ? i0 + lane : lane == CHUNK ? i0 - 1 : i0 + CHUNK;
+    const bool have = (lane < count || lane >= CHUNK) && lane <= CHUNK + 1 && at >= 0 && at < s.tokens;
+    if (have) {
+        k = ldg(s.key + at);
+        p = ldg(s.pos + at);
+    }
+    run_sums<T, ACC, ACC ? CHUNK / 2 : CHUNK>(s, cols, chunk, k, p);
 }
 
 // The run that begins in a chunk and goes on into later ones: its partial rows in order.
@@ -393,22 +415,32 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void join_runs_kernel(RunSum s) {
     }
     const uint32_t end = (uint32_t)((lo - 1) / CHUNK);      // last chunk of the run
     const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t c = (int64_t)(blockIdx.x - chunk * s.col_tiles) * COLS + lane * 8;
-    const int n = (int)max((int64_t)0, min((int64_t)8, s.dim - c));
+    const Cols cols = lane_cols(blockIdx.x - chunk * s.col_tiles, s.dim);
+    const int64_t c = cols.n > 0 ? cols.c : 0;              // partial rows are padded to eights
     floatx8 acc = {};
-    for (uint32_t j = chunk + wv; j <= end; j += JOIN_WAVES) {
-        const float* p = (j == chunk ? s.last : s.first) + (int64_t)j * s.dim + c;
-        acc += Vec8<float>::get(load8_n(p, n));
-    }
+    for (uint32_t j = chunk + wv; j <= end; j += JOIN_WAVES)
+        acc += Vec8<float>::get(load8((j == chunk ? s.last : s.first) + (int64_t)j * s.pitch + c));
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[wv][lane * 8 + i] = acc[i];
     __syncthreads();
-    if (wv == 0 && n > 0) {
+    if (wv == 0 && cols.n > 0) {
         for (int w = 1; w < JOIN_WAVES; ++w)
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[i] += part[w][lane * 8 + i];
-        put_row(s, key, c, n, acc);
+        acc *= s.scale;
+        float* g = s.g + (int64_t)key * s.ldg + cols.c;
+        if (s.accumulate) acc += Vec8<float>::get(load8_n(g, cols.n));
+        store8_n(g, Vec8<float>::put(acc), cols.n);
     }
+}
+
+template <class T>
+void run_sums_of(const RunSum& r, uint32_t waves, hipStream_t stream) {
+    const dim3 grid((waves + 3) / 4);
+    if (r.accumulate)
+        S4_LAUNCH((run_sums_kernel<T, true>), grid, dim3(256), 0, stream, r);
+    else
+        S4_LAUNCH((run_sums_kernel<T, false>), grid, dim3(256), 0, stream, r);
 }
 
 struct GradPlan {
@@ -438,8 +470,8 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t dim) {
         p.off_pos[i] = take((size_t)tokens * 4);
     }
     p.off_hist = take(p.small ? 0 : (size_t)p.nblk * BINS * 4);
-    p.off_first = take((size_t)p.chunks * dim * 4);
-    p.off_last = take((size_t)p.chunks * dim * 4);
+    p.off_first = take((size_t)p.chunks * ((dim + 7) / 8 * 8) * 4);
+    p.off_last = take((size_t)p.chunks * ((dim + 7) / 8 * 8) * 4);
     p.total = at;
     return p;
 }
@@ -514,6 +546,7 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
     r.last = (float*)(ws + p.off_last);
     r.tokens = e.tokens;
     r.dim = e.dim;
+    r.pitch = (e.dim + 7) / 8 * 8;
     r.lddout = e.lddout;
     r.ldg = e.ldg;
     r.vocab = (uint32_t)e.vocab;
@@ -523,9 +556,9 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
     r.accumulate = e.accumulate;
     const uint32_t waves = r.chunks * r.col_tiles;
     switch (dtype) {
-        case SHAMPOO4_BF16: S4_LAUNCH(run_sums_kernel<__bf16>, dim3((waves + 3) / 4), dim3(256), 0, stream, r); break;
-        case SHAMPOO4_F16: S4_LAUNCH(run_sums_kernel<_Float16>, dim3((waves + 3) / 4), dim3(256), 0, stream, r); break;
-        default: S4_LAUNCH(run_sums_kernel<float>, dim3((waves + 3) / 4), dim3(256), 0, stream, r);
+        case SHAMPOO4_BF16: run_sums_of<__bf16>(r, waves, stream); break;
+        case SHAMPOO4_F16: run_sums_of<_Float16>(r, waves, stream); break;
+        default: run_sums_of<float>(r, waves, stream);
     }
     if (r.chunks > 1) S4_LAUNCH(join_runs_kernel, dim3(waves), dim3(64 * JOIN_WAVES), 0, stream, r);
     return hipGetLastError();

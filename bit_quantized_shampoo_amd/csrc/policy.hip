@@ -42,13 +42,6 @@ __device__ __forceinline__ float log_prob(float zy, float base, float s) {
     return LN2 * (fmaf(zy, LOG2E, -base) - __builtin_amdgcn_logf(s));
 }
 
-// Keeps the compiler from carrying eight unpacked values per vector from one use of a
-// register-resident row to the next (they would take twice the row's registers).
-template <class R>
-__device__ __forceinline__ void unpack_again(R& r) {
-    if constexpr (sizeof(R) == 16) asm volatile("" : "+v"(r));
-}
-
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));

@@ -88,6 +88,24 @@ __device__ __forceinline__ typename Vec8<T>::Raw load8_n(const T* p, int n) {
     }
     return r;
 }
+// Elements c .. c + 7 of a row of `cols`, zero beyond its end, without a branch (a load
+// under one is waited for before the next can be issued): indexes are clamped into the row
+// and what they bring in from there is masked.
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::Raw load8_clamped(const T* row, int64_t c, int64_t cols) {
+    typename Vec8<T>::Raw r = {};
+    const int n = (int)max((int64_t)0, min((int64_t)8, cols - c));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t i = min(c + j, cols - 1);
+        const uint32_t keep = j < n ? 0xffffffffu : 0u;
+        if constexpr (sizeof(T) == 4)
+            r[j] = ldg((const uint32_t*)row + i) & keep;
+        else
+            r[j >> 1] |= ((uint32_t)ldg((const uint16_t*)row + i) & keep) << (16 * (j & 1));
+    }
+    return r;
+}
 template <class T>
 __device__ __forceinline__ void store8_n(T* p, typename Vec8<T>::Raw v, int n) {
     if (n >= 8) {
@@ -104,9 +122,12 @@ __device__ __forceinline__ void store8_n(T* p, typename Vec8<T>::Raw v, int n) {
         }
 }
 
-// Eight values rounded to T and back: what a consumer of the stored elements reads.
-template <class T>
-__device__ __forceinline__ floatx8 round8(floatx8 f) { return Vec8<T>::get(Vec8<T>::put(f)); }
+// Keeps the compiler from carrying unpacked values from one use of raw registers to the next
+// (they would take twice the registers).
+template <class R>
+__device__ __forceinline__ void unpack_again(R& r) {
+    if constexpr (sizeof(R) == 16) asm volatile("" : "+v"(r));
+}
 
 // -- the 8-bit checkpoint ----------------------------------------------------------------
 
