@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void embedding_kernel(Embed e, uint32_t nvec, 
         const int n = (int)min((int64_t)8, e.dim - c);
         typename Vec8<T>::Raw r = {};
         if (id >= 0 && id < e.vocab) {
-            r = load8_n((const T*)e.table + id * e.ldtable + c, n);
+            r = load8_edge((const T*)e.table + id * e.ldtable, c, e.dim);
             r = Vec8<T>::put(Vec8<T>::get(r) * e.scale);
         }
         store8_n((T*)e.out + (int64_t)t * e.ldout + c, r, n);
@@ -311,25 +311,23 @@ struct RunSum {
     int accumulate;
 };
 
-// A lane's eight columns of a row: whole vectors where no lane of the wave has its columns end
-// inside them, else element by element; clamped into the row, so that no load is under a
-// lane's own condition.
+// A lane's eight columns of a row; `whole`: no lane of the wave crosses the row's end.
 struct Cols {
     int64_t c, dim;
     int n;                    // valid columns, 0..8
-    bool vectors;
+    bool whole;
 };
 __device__ __forceinline__ Cols lane_cols(int64_t tile, int64_t dim) {
     Cols k;
     k.c = tile * COLS + (threadIdx.x & 63) * 8;
     k.dim = dim;
     k.n = (int)max((int64_t)0, min((int64_t)8, dim - k.c));
-    k.vectors = dim >= 8 && __all(k.n == 8 || k.n == 0);
+    k.whole = dim >= 8 && __all(k.n == 8 || k.n == 0);
     return k;
 }
 template <class T>
 __device__ __forceinline__ typename Vec8<T>::Raw load_cols(const T* row, const Cols& k) {
-    return k.vectors ? load8(row + (k.n ? k.c : 0)) : load8_clamped(row, k.c, k.dim);
+    return k.whole ? load8(row + (k.n ? k.c : 0)) : load8_edge(row, k.c, k.dim);
 }
 
 // Sums of a chunk's runs, BATCH positions in flight at a time; with ACC the rows of G that a
@@ -429,7 +427,7 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void join_runs_kernel(RunSum s) {
             for (int i = 0; i < 8; ++i) acc[i] += part[w][lane * 8 + i];
         acc *= s.scale;
         float* g = s.g + (int64_t)key * s.ldg + cols.c;
-        if (s.accumulate) acc += Vec8<float>::get(load8_n(g, cols.n));
+        if (s.accumulate) acc += Vec8<float>::get(load8_edge(s.g + (int64_t)key * s.ldg, cols.c, s.dim));
         store8_n(g, Vec8<float>::put(acc), cols.n);
     }
 }

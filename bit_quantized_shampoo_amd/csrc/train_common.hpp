@@ -68,35 +68,40 @@ __device__ __forceinline__ void store8(T* p, typename Vec8<T>::Raw v) {
     using G = __attribute__((address_space(1))) typename Vec8<T>::Mem;
     *(G*)p = v;
 }
-// The first n (0..8) of eight elements; the others are zero, and not accessed.
+// Elements s .. 7 moved to places 0 .. 7 - s, zeros behind them (s = 0 .. 8).
 template <class T>
-__device__ __forceinline__ typename Vec8<T>::Raw load8_n(const T* p, int n) {
-    if (n >= 8) return load8(p);
-    typename Vec8<T>::Raw r = {};
-    if constexpr (sizeof(T) == 4) {
-        for (int i = 0; i < n; ++i) {
-            const uint32_t b = ldg((const uint32_t*)p + i);
+__device__ __forceinline__ typename Vec8<T>::Raw shift_down(typename Vec8<T>::Raw r, int s) {
+    constexpr int N = sizeof(r) / 4;
+    int d = s;                                               // in dwords
+    if constexpr (N == 4) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = i == j ? b : r[j];
+        for (int i = 0; i < N; ++i) {
+            const uint32_t up = i + 1 < N ? r[(i + 1) % N] : 0u;
+            r[i] = s & 1 ? __builtin_amdgcn_alignbit(up, r[i], 16) : r[i];
         }
-    } else {
-        for (int i = 0; i < n; ++i) {
-            const uint32_t b = (uint32_t)ldg((const uint16_t*)p + i) << (16 * (i & 1));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r[j] |= (i >> 1) == j ? b : 0u;
-        }
+        d = s >> 1;
     }
+#pragma unroll
+    for (int step = 1; step <= N; step *= 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t up = i + step < N ? r[(i + step) % N] : 0u;
+            r[i] = d & step ? up : r[i];
+        }
     return r;
 }
-// Elements c .. c + 7 of a row of `cols`, zero beyond its end, without a branch (a load
-// under one is waited for before the next can be issued): indexes are clamped into the row
-// and what they bring in from there is masked.
+
+// Elements c .. c + 7 of a row of `cols` >= 1, zeros beyond its end.  No load is under a lane's
+// own condition (it would be waited for before the next is issued): a vector that crosses
+// the end is loaded eight from it and shifted, and a row of fewer than eight element by
+// element, with indexes clamped into it.
 template <class T>
-__device__ __forceinline__ typename Vec8<T>::Raw load8_clamped(const T* row, int64_t c, int64_t cols) {
-    typename Vec8<T>::Raw r = {};
+__device__ __forceinline__ typename Vec8<T>::Raw load8_edge(const T* row, int64_t c, int64_t cols) {
     const int n = (int)max((int64_t)0, min((int64_t)8, cols - c));
+    if (cols >= 8) return shift_down<T>(load8(row + min(c, cols - 8)), 8 - n);
+    typename Vec8<T>::Raw r = {};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 7; ++j) {
         const int64_t i = min(c + j, cols - 1);
         const uint32_t keep = j < n ? 0xffffffffu : 0u;
         if constexpr (sizeof(T) == 4)
@@ -106,20 +111,45 @@ __device__ __forceinline__ typename Vec8<T>::Raw load8_clamped(const T* row, int
     }
     return r;
 }
+
+// The first n (0..8) of eight elements: the whole vector, or pieces of four, two and one.
 template <class T>
 __device__ __forceinline__ void store8_n(T* p, typename Vec8<T>::Raw v, int n) {
     if (n >= 8) {
         store8(p, v);
         return;
     }
+    constexpr int N = sizeof(v) / 4;
+    typedef uint32_t H4 __attribute__((ext_vector_type(N / 2)));
+    typedef H4 M4 __attribute__((aligned(sizeof(T))));
+    if (n & 4) {
+        using G = __attribute__((address_space(1))) M4;
+        H4 h;
 #pragma unroll
-    for (int i = 0; i < 7; ++i)
-        if (i < n) {
-            if constexpr (sizeof(T) == 4)
-                stg((uint32_t*)p + i, v[i]);
-            else
-                stg((uint16_t*)p + i, (uint16_t)(v[i >> 1] >> (16 * (i & 1))));
+        for (int i = 0; i < N / 2; ++i) h[i] = v[i];
+        *(G*)p = h;
+        v = shift_down<T>(v, 4);
+        p += 4;
+    }
+    if (n & 2) {
+        if constexpr (sizeof(T) == 4) {
+            typedef u32x2 M2 __attribute__((aligned(4)));
+            using G = __attribute__((address_space(1))) M2;
+            *(G*)p = u32x2{v[0], v[1]};
+        } else {
+            typedef uint32_t M2 __attribute__((aligned(2)));
+            using G = __attribute__((address_space(1))) M2;
+            *(G*)p = v[0];
         }
+        v = shift_down<T>(v, 2);
+        p += 2;
+    }
+    if (n & 1) {
+        if constexpr (sizeof(T) == 4)
+            stg((uint32_t*)p, v[0]);
+        else
+            stg((uint16_t*)p, (uint16_t)v[0]);
+    }
 }
 
 // Keeps the compiler from carrying unpacked values from one use of raw registers to the next

@@ -268,17 +268,19 @@ __global__ __launch_bounds__(64 * WM * WN) void wgrad_kernel(WGrad w, int tiles_
 #pragma unroll
         for (int i = 0; i < VA; ++i) {
             const int64_t row = k + arow + i * AR;
-            const int n = (int)max((int64_t)0, min((int64_t)8, w.n - m0 - acol));
-            a[i] = load8_n((const T*)w.dy + row * w.lddy + m0 + acol, row < r1 ? n : 0);
+            a[i] = load8_edge((const T*)w.dy + min(row, r1 - 1) * w.lddy, m0 + acol, w.n);
+            a[i] &= row < r1 ? 0xffffffffu : 0u;
         }
 #pragma unroll
         for (int i = 0; i < KS / 32; ++i)
-            e[i] = k + 32 * i < r1 ? ldg((const u32x2*)(w.scales + (k / 32 + i) * pitch + bn)) : u32x2{0, 0};
+            e[i] = ldg((const u32x2*)(w.scales + min(k / 32 + i, (r1 - 1) / 32) * pitch + bn));
 #pragma unroll
         for (int i = 0; i < VB; ++i) {
             const int64_t row = k + brow + i * BR;
-            c[i] = u32x2{0, 0};
-            if (row < r1) c[i] = ldg((const u32x2*)(w.codes + row * pitch + bn));
+            // past the checkpoint's last block: codes 0, and a scale that is finite
+            const bool have = row < (r1 + 31) / 32 * 32;
+            c[i] = ldg((const u32x2*)(w.codes + (have ? row : 0) * pitch + bn));
+            c[i] &= have ? 0xffffffffu : 0u;
         }
         __syncthreads();
 #pragma unroll
