@@ -4,18 +4,18 @@
 //
 // Gradient: G[v] = scale * sum of dout[t] over the tokens t with id v.
 //  1. The positions are sorted by id, stably: least significant digit first, digits of up to
-//     9 bits (two passes up to 262143 words).  A wave ranks 64 ids at a time: nine ballots
-//     give each lane the lanes that share its digit, its rank among them and their number.
-//     Up to SMALL_T tokens one workgroup sorts in LDS, in one launch; beyond, a pass is two
-//     launches over blocks of SORT_TILE tokens (digit counts, then ranks and scatter).
+//     9 bits.  A wave ranks 64 ids at a time: a ballot a bit gives each lane the lanes that
+//     share its digit, its rank among them and their number.  Up to SMALL_T tokens it is one
+//     launch, each workgroup sorting a range of ids in LDS; beyond, a pass is two launches
+//     over blocks of SORT_TILE tokens (digit counts, then ranks and scatter).
 //     Without accumulation the other workgroups of these launches write G's zeros: the fill
-//     is bound by HBM and the sort by latency, so the sort costs next to nothing beside it.
+//     is bound by HBM and the sort by latency, so the sort costs little beside it.
 //  2. Sums over chunks of CHUNK sorted positions, one wave for 512 columns of a chunk: a run
 //     of equal ids inside a chunk is stored as a row of G; a run that crosses the chunk's
 //     ends goes to a partial row.  Every load address is known before the first sum, so
 //     eight rows are in flight.
-//  3. Runs over several chunks: one workgroup per run and 512 columns adds the partial rows,
-//     eight waves each every eighth, joined in a fixed order.
+//  3. Runs over several chunks: a wave adds a short run's partial rows, a workgroup of eight
+//     waves a long one's, each every eighth, joined in a fixed order.
 // The order of every sum follows from the ids alone: no floating atomics.
 #include <algorithm>
 
@@ -28,7 +28,7 @@ namespace {
 
 constexpr int RADIX_BITS = 9;                // most bits of a digit
 constexpr int BINS = 1 << RADIX_BITS;
-constexpr int SMALL_T = 16384;               // one workgroup: 16 waves of up to 16 rounds
+constexpr int SMALL_T = 16384;               // one launch: 16 waves of up to 16 rounds
 constexpr int SMALL_WAVES = 16;
 constexpr int TILE_WAVES = 8;
 constexpr int TILE_ROUNDS = 8;
@@ -136,15 +136,20 @@ __device__ __forceinline__ void wave_ranks(const uint32_t (&digit)[ROUNDS], cons
 
 // Turns cnt [waves][bins] into each wave's first place per digit, and returns through
 // `tot` (LDS, bins) each digit's first place in the workgroup's own order.
-__device__ __forceinline__ void digit_places(uint32_t* cnt, int waves, int bins, uint32_t* tot, uint32_t* wsum) {
+template <int WAVES>
+__device__ __forceinline__ void digit_places(uint32_t* cnt, int bins, uint32_t* tot, uint32_t* wsum) {
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     uint32_t s = 0;
-    if (tid < bins)
-        for (int w = 0; w < waves; ++w) {
-            const uint32_t c = cnt[w * BINS + tid];
+    if (tid < bins) {
+        uint32_t c[WAVES];
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) c[w] = cnt[w * BINS + tid];
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
             cnt[w * BINS + tid] = s;
-            s += c;
+            s += c[w];
         }
+    }
     uint32_t inc = s;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -159,49 +164,88 @@ __device__ __forceinline__ void digit_places(uint32_t* cnt, int waves, int bins,
     __syncthreads();
 }
 
-// Up to SMALL_T tokens: workgroup 0 sorts (id, position) packed in one word (`pos_bits` low
-// bits of position) in LDS; the others fill zeros.
+// Up to SMALL_T tokens: workgroup k < parts sorts the ids of the k-th range of `range` ids;
+// the others fill zeros.  A sorting workgroup reads every id: it counts those below its
+// range, which gives the place of its output without a word from the others, and takes its
+// own, in order, into LDS (all of them, if all are in one range), as (id - first of the
+// range, position) in one word with `pos_bits` low bits of position.
 __global__ __launch_bounds__(1024) void sort_small_kernel(const void* ids, int id64, int64_t vocab, int tokens,
-                                                          int passes, int bits, int pos_bits, uint32_t* skey,
-                                                          uint32_t* spos, Fill fill) {
+                                                          int parts, uint32_t range, int passes, int bits,
+                                                          int pos_bits, uint32_t* skey, uint32_t* spos, Fill fill) {
     __shared__ uint32_t buf[SMALL_T];
     __shared__ uint32_t cnt[SMALL_WAVES * BINS];
     __shared__ uint32_t tot[BINS];
-    __shared__ uint32_t wsum[SMALL_WAVES];
-    if (blockIdx.x > 0) {
-        fill_zeros(fill, blockIdx.x - 1, gridDim.x - 1);
+    __shared__ uint32_t wsum[SMALL_WAVES], wbelow[SMALL_WAVES];
+    if ((int)blockIdx.x >= parts) {
+        fill_zeros(fill, blockIdx.x - parts, gridDim.x - parts);
         return;
     }
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int rounds = (tokens + 1023) / 1024;
     const int bins = 1 << bits;
+    const uint32_t lo = blockIdx.x * range;
     uint32_t item[16], digit[16], rank[16];
     bool live[16];
+    int rounds = (tokens + 1023) / 1024;
+    // item number (wave, round, lane): each wave a contiguous piece; every load is issued
+    // before the first is looked at, so none is under a condition
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
         const int i = (wv * rounds + r) * 64 + lane;
         live[r] = r < rounds && i < tokens;
-        item[r] = live[r] ? key_at(ids, id64, vocab, i) << pos_bits | (uint32_t)i : 0u;
+        item[r] = key_at(ids, id64, vocab, min(i, tokens - 1));
     }
+    uint32_t mine = 0, below = 0;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        if (r >= rounds) {
+            live[r] = false;
+            continue;
+        }
+        below += __popcll(__ballot(live[r] && item[r] < lo));
+        live[r] = live[r] && item[r] - lo < range;           // below: wraps to a large number
+        const uint64_t m = __ballot(live[r]);
+        rank[r] = mine + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
+        mine += __popcll(m);
+    }
+    if (lane == 0) {
+        wsum[wv] = mine;
+        wbelow[wv] = below;
+    }
+    __syncthreads();
+    uint32_t at = 0, n = 0, out = 0;
+#pragma unroll
+    for (int w = 0; w < SMALL_WAVES; ++w) {
+        const uint32_t c = wsum[w];
+        at += w < wv ? c : 0u;
+        n += c;
+        out += wbelow[w];
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+        if (live[r]) buf[at + rank[r]] = (item[r] - lo) << pos_bits | (uint32_t)((wv * rounds + r) * 64 + lane);
+    rounds = ((int)n + 1023) / 1024;
     for (int p = 0; p < passes; ++p) {
-        for (int i = tid; i < SMALL_WAVES * BINS; i += 1024) cnt[i] = 0;
+        for (int i = lane; i < bins; i += 64) cnt[wv * BINS + i] = 0;
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            if (p > 0 && live[r]) item[r] = buf[(wv * rounds + r) * 64 + lane];
+            const int i = (wv * rounds + r) * 64 + lane;
+            live[r] = r < rounds && i < (int)n;
+            if (r >= rounds) continue;
+            item[r] = buf[min(i, SMALL_T - 1)];
             digit[r] = (item[r] >> (pos_bits + p * bits)) & (uint32_t)(bins - 1);
         }
         wave_ranks<16>(digit, live, bits, cnt + wv * BINS, rank, rounds);
         __syncthreads();
-        digit_places(cnt, SMALL_WAVES, bins, tot, wsum);
+        digit_places<SMALL_WAVES>(cnt, bins, tot, wsum);
 #pragma unroll
         for (int r = 0; r < 16; ++r)
             if (live[r]) buf[tot[digit[r]] + cnt[wv * BINS + digit[r]] + rank[r]] = item[r];
         __syncthreads();
     }
-    for (int i = tid; i < tokens; i += 1024) {
-        stg(skey + i, buf[i] >> pos_bits);
-        stg(spos + i, buf[i] & ((1u << pos_bits) - 1));
+    for (int i = tid; i < (int)n; i += 1024) {
+        stg(skey + out + i, lo + (buf[i] >> pos_bits));
+        stg(spos + out + i, buf[i] & ((1u << pos_bits) - 1));
     }
 }
 
@@ -226,14 +270,15 @@ __global__ __launch_bounds__(512) void sort_count_kernel(SortPass s, Fill fill) 
     h[tid] = 0;
     __syncthreads();
     const int64_t i0 = (int64_t)blockIdx.x * SORT_TILE;
+    uint32_t key[SORT_TILE / 512];
 #pragma unroll
     for (int r = 0; r < SORT_TILE / 512; ++r) {
-        const int64_t i = i0 + r * 512 + tid;
-        if (i < s.tokens) {
-            const uint32_t k = s.ids ? key_at(s.ids, s.id64, s.vocab, i) : ldg(s.key + i);
-            atomicAdd(&h[(k >> s.shift) & (uint32_t)(bins - 1)], 1u);
-        }
+        const int64_t i = min(i0 + r * 512 + tid, s.tokens - 1);
+        key[r] = s.ids ? key_at(s.ids, s.id64, s.vocab, i) : ldg(s.key + i);
     }
+#pragma unroll
+    for (int r = 0; r < SORT_TILE / 512; ++r)
+        if (i0 + r * 512 + tid < s.tokens) atomicAdd(&h[(key[r] >> s.shift) & (uint32_t)(bins - 1)], 1u);
     __syncthreads();
     if (tid < bins) stg(s.hist + (int64_t)blockIdx.x * bins + tid, h[tid]);
 }
@@ -248,15 +293,16 @@ __global__ __launch_bounds__(512) void sort_scatter_kernel(SortPass s, Fill fill
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, bins = 1 << s.bits;
     for (int i = tid; i < TILE_WAVES * BINS; i += 512) cnt[i] = 0;
     __syncthreads();
-    uint32_t key[TILE_ROUNDS], digit[TILE_ROUNDS], rank[TILE_ROUNDS];
+    uint32_t key[TILE_ROUNDS], pos[TILE_ROUNDS], digit[TILE_ROUNDS], rank[TILE_ROUNDS];
     bool live[TILE_ROUNDS];
     const int64_t i0 = (int64_t)blockIdx.x * SORT_TILE + wv * TILE_ROUNDS * 64 + lane;
 #pragma unroll
     for (int r = 0; r < TILE_ROUNDS; ++r) {
         const int64_t i = i0 + r * 64;
         live[r] = i < s.tokens;
-        key[r] = 0;
-        if (live[r]) key[r] = s.ids ? key_at(s.ids, s.id64, s.vocab, i) : ldg(s.key + i);
+        const int64_t in = min(i, s.tokens - 1);
+        key[r] = s.ids ? key_at(s.ids, s.id64, s.vocab, in) : ldg(s.key + in);
+        pos[r] = s.ids ? (uint32_t)in : ldg(s.pos + in);
         digit[r] = (key[r] >> s.shift) & (uint32_t)(bins - 1);
     }
     wave_ranks<TILE_ROUNDS>(digit, live, s.bits, cnt + wv * BINS, rank, TILE_ROUNDS);
@@ -291,10 +337,9 @@ __global__ __launch_bounds__(512) void sort_scatter_kernel(SortPass s, Fill fill
 #pragma unroll
     for (int r = 0; r < TILE_ROUNDS; ++r)
         if (live[r]) {
-            const int64_t i = i0 + r * 64;
             const uint32_t at = cnt[wv * BINS + digit[r]] + rank[r];
             stg(s.key_out + at, key[r]);
-            stg(s.pos_out + at, s.ids ? (uint32_t)i : ldg(s.pos + i));
+            stg(s.pos_out + at, pos[r]);
         }
 }
 
@@ -396,39 +441,85 @@ __global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
     run_sums<T, ACC, ACC ? CHUNK / 2 : CHUNK>(s, cols, chunk, k, p);
 }
 
-// The run that begins in a chunk and goes on into later ones: its partial rows in order.
+// Partial rows from, from + step, .. up to `end` of the run that begins in `chunk`, in order,
+// four in flight.
+__device__ __forceinline__ floatx8 add_parts(const RunSum& s, uint32_t chunk, uint32_t from, uint32_t step, uint32_t end,
+                                             int64_t c) {
+    floatx8 acc = {};
+    for (uint32_t j = from; j <= end; j += 4 * step) {
+        typename Vec8<float>::Raw r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t k = min(j + i * step, end);
+            r[i] = load8((k == chunk ? s.last : s.first) + (int64_t)k * s.pitch + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (j + i * step <= end) acc += Vec8<float>::get(r[i]);
+    }
+    return acc;
+}
+
+// Runs over several chunks: the partial rows of one, in order.  A wave looks at one chunk and
+// 512 columns, and adds a short run by itself; the waves of a workgroup share a long one,
+// each taking every JOIN_WAVES-th partial row, joined in the order of the waves.
 __global__ __launch_bounds__(64 * JOIN_WAVES) void join_runs_kernel(RunSum s) {
     __shared__ float part[JOIN_WAVES][COLS];
-    const uint32_t chunk = blockIdx.x / s.col_tiles;
-    const int64_t i0 = (int64_t)chunk * CHUNK, i1 = i0 + CHUNK;
-    if (i1 >= s.tokens) return;
-    const uint32_t key = ldg(s.key + i1 - 1);
-    if (key >= s.vocab || ldg(s.key + i1) != key) return;
-    if (ldg(s.key + i0) == key && i0 > 0 && ldg(s.key + i0 - 1) == key) return;    // began before
-    // the run's end: the first sorted position after i1 with another key
-    int64_t lo = i1 + 1, hi = s.tokens;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (ldg(s.key + mid) == key) lo = mid + 1; else hi = mid;
-    }
-    const uint32_t end = (uint32_t)((lo - 1) / CHUNK);      // last chunk of the run
+    __shared__ uint32_t ends[JOIN_WAVES];
     const int wv = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const Cols cols = lane_cols(blockIdx.x - chunk * s.col_tiles, s.dim);
-    const int64_t c = cols.n > 0 ? cols.c : 0;              // partial rows are padded to eights
-    floatx8 acc = {};
-    for (uint32_t j = chunk + wv; j <= end; j += JOIN_WAVES)
-        acc += Vec8<float>::get(load8((j == chunk ? s.last : s.first) + (int64_t)j * s.pitch + c));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) part[wv][lane * 8 + i] = acc[i];
-    __syncthreads();
-    if (wv == 0 && cols.n > 0) {
-        for (int w = 1; w < JOIN_WAVES; ++w)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += part[w][lane * 8 + i];
+    const uint32_t wave = blockIdx.x * JOIN_WAVES + wv;
+    uint32_t chunk = wave / s.col_tiles, key = 0, end = 0;   // end: last chunk of the run, 0: none
+    const int64_t i0 = (int64_t)chunk * CHUNK, i1 = i0 + CHUNK;
+    if (i1 < s.tokens) {
+        // the keys around the chunk's ends, loaded together
+        const uint32_t last = ldg(s.key + i1 - 1), after = ldg(s.key + i1), first = ldg(s.key + i0);
+        const uint32_t before = ldg(s.key + max(i0 - 1, (int64_t)0));
+        const bool begun_before = first == last && i0 > 0 && before == last;
+        if (last < s.vocab && after == last && !begun_before) {
+            key = last;
+            // the chunks after this one that begin with the same id, 64 at a time
+            end = chunk;
+            uint64_t same;
+            do {
+                const int64_t i = ((int64_t)end + 1 + lane) * CHUNK;
+                same = __ballot(i < s.tokens && ldg(s.key + min(i, s.tokens - 1)) == key);
+                end += ~same ? (uint32_t)__builtin_ctzll(~same) : 64u;
+            } while (~same == 0);
+        }
+    }
+    const auto put = [&](const Cols& cols, uint32_t row, floatx8 acc) {
+        if (cols.n == 0) return;
         acc *= s.scale;
-        float* g = s.g + (int64_t)key * s.ldg + cols.c;
-        if (s.accumulate) acc += Vec8<float>::get(load8_edge(s.g + (int64_t)key * s.ldg, cols.c, s.dim));
-        store8_n(g, Vec8<float>::put(acc), cols.n);
+        float* g = s.g + (int64_t)row * s.ldg;
+        if (s.accumulate) acc += Vec8<float>::get(load8_edge(g, cols.c, s.dim));
+        store8_n(g + cols.c, Vec8<float>::put(acc), cols.n);
+    };
+    const bool is_long = end > chunk + 2 * JOIN_WAVES;
+    if (end && !is_long) {
+        const Cols cols = lane_cols(wave - chunk * s.col_tiles, s.dim);
+        const int64_t c = cols.n > 0 ? cols.c : 0;           // partial rows are padded to eights
+        put(cols, key, add_parts(s, chunk, chunk, 1, end, c));
+    }
+    if (lane == 0) ends[wv] = is_long ? end : 0;
+    __syncthreads();
+    for (int v = 0; v < JOIN_WAVES; ++v) {
+        const uint32_t last = ends[v];
+        if (last == 0) continue;                             // the same for every thread
+        const uint32_t w = blockIdx.x * JOIN_WAVES + v;
+        chunk = w / s.col_tiles;
+        const Cols cols = lane_cols(w - chunk * s.col_tiles, s.dim);
+        const int64_t c = cols.n > 0 ? cols.c : 0;
+        floatx8 acc = add_parts(s, chunk, chunk + wv, JOIN_WAVES, last, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[wv][i * 64 + lane] = acc[i];
+        __syncthreads();
+        if (wv == 0) {
+            for (int u = 1; u < JOIN_WAVES; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) acc[i] += part[u][i * 64 + lane];
+            put(cols, ldg(s.key + (int64_t)(chunk + 1) * CHUNK), acc);
+        }
+        __syncthreads();
     }
 }
 
@@ -443,7 +534,8 @@ void run_sums_of(const RunSum& r, uint32_t waves, hipStream_t stream) {
 
 struct GradPlan {
     int64_t chunks, nblk;
-    int bits, passes, digit, pos_bits;
+    int bits, passes, digit, pos_bits, parts;
+    uint32_t range;           // ids a part of the small sort
     bool small;
     size_t off_key[2], off_pos[2], off_hist, off_first, off_last, total;
 };
@@ -451,11 +543,16 @@ GradPlan grad_plan(int64_t tokens, int64_t vocab, int64_t dim) {
     GradPlan p;
     p.chunks = (tokens + CHUNK - 1) / CHUNK;
     p.bits = bit_length((uint64_t)vocab);                    // keys 0 .. vocab
+    p.pos_bits = bit_length((uint64_t)(tokens > 0 ? tokens - 1 : 0));
+    // a part for every 512 tokens: 16384 tokens into 65536 rows sort in 33 us in one part
+    p.parts = (int)std::min<int64_t>(16, std::max<int64_t>(1, tokens / 512));
+    p.range = (uint32_t)((vocab + p.parts) / p.parts);
+    const int part_bits = std::max(1, bit_length(p.range - 1));
+    // id and position in one word: larger tables sort in blocks, whatever the tokens
+    p.small = tokens <= SMALL_T && part_bits + p.pos_bits <= 32;
+    if (p.small) p.bits = part_bits;
     p.passes = (p.bits + RADIX_BITS - 1) / RADIX_BITS;
     p.digit = (p.bits + p.passes - 1) / p.passes;
-    p.pos_bits = bit_length((uint64_t)(tokens > 0 ? tokens - 1 : 0));
-    // id and position in one word: larger tables sort in blocks, whatever the tokens
-    p.small = tokens <= SMALL_T && p.bits + p.pos_bits <= 32;
     p.nblk = (tokens + SORT_TILE - 1) / SORT_TILE;
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -507,8 +604,9 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
     if (e.tokens == 0 || p.small) {
         skey = (uint32_t*)(ws + p.off_key[0]);
         spos = (uint32_t*)(ws + p.off_pos[0]);
-        S4_LAUNCH(sort_small_kernel, dim3(1 + fill_blocks(1)), dim3(1024), 0, stream, e.ids, e.id64, e.vocab,
-                  (int)e.tokens, p.passes, p.digit, p.pos_bits, skey, spos, fill);
+        const int parts = e.tokens == 0 ? 0 : p.parts;       // no tokens: nothing is read
+        S4_LAUNCH(sort_small_kernel, dim3(parts + fill_blocks(1)), dim3(1024), 0, stream, e.ids, e.id64, e.vocab,
+                  (int)e.tokens, parts, p.range, p.passes, p.digit, p.pos_bits, skey, spos, fill);
     } else {
         fill.parts = 2 * p.passes;
         const uint32_t nf = fill_blocks(fill.parts);
@@ -558,7 +656,8 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
         case SHAMPOO4_F16: run_sums_of<_Float16>(r, waves, stream); break;
         default: run_sums_of<float>(r, waves, stream);
     }
-    if (r.chunks > 1) S4_LAUNCH(join_runs_kernel, dim3(waves), dim3(64 * JOIN_WAVES), 0, stream, r);
+    if (r.chunks > 1)
+        S4_LAUNCH(join_runs_kernel, dim3((waves + JOIN_WAVES - 1) / JOIN_WAVES), dim3(64 * JOIN_WAVES), 0, stream, r);
     return hipGetLastError();
 }
 
