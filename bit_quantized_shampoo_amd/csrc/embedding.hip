@@ -10,10 +10,9 @@
 //     over blocks of SORT_TILE tokens (digit counts, then ranks and scatter).
 //     Without accumulation the other workgroups of these launches write G's zeros: the fill
 //     is bound by HBM and the sort by latency, so the sort costs little beside it.
-//  2. Sums over chunks of CHUNK sorted positions, one wave for 512 columns of a chunk: a run
-//     of equal ids inside a chunk is stored as a row of G; a run that crosses the chunk's
-//     ends goes to a partial row.  Every load address is known before the first sum, so
-//     eight rows are in flight.
+//  2. Sums of runs of equal ids, cut at every CHUNK sorted positions: one wave per piece (short
+//     lists) or per chunk, and 512 columns.  A run inside a chunk is stored as a row of G; a piece of a longer one goes
+//     to a partial row.
 //  3. Runs over several chunks: a wave adds a short run's partial rows, a workgroup of eight
 //     waves a long one's, each every eighth, joined in a fixed order.
 // The order of every sum follows from the ids alone: no floating atomics.
@@ -164,11 +163,42 @@ __device__ __forceinline__ void digit_places(uint32_t* cnt, int bins, uint32_t* 
     __syncthreads();
 }
 
+// The passes of a small sort: n <= 1024 R items in buf, by the `passes` digits of `bits` bits
+// from bit `shift` on.  Items are in registers between the barriers of a pass, so buf is
+// sorted in place.
+template <int R>
+__device__ void sort_in_lds(uint32_t* buf, int n, int shift, int passes, int bits, uint32_t* cnt, uint32_t* tot,
+                            uint32_t* wsum) {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, bins = 1 << bits;
+    const int rounds = (n + 1023) / 1024;
+    uint32_t item[R], digit[R], rank[R];
+    bool live[R];
+    for (int p = 0; p < passes; ++p) {
+        for (int i = lane; i < bins; i += 64) cnt[wv * BINS + i] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = (wv * rounds + r) * 64 + lane;
+            live[r] = r < rounds && i < n;
+            item[r] = buf[min(i, SMALL_T - 1)];
+            digit[r] = (item[r] >> (shift + p * bits)) & (uint32_t)(bins - 1);
+        }
+        wave_ranks<R>(digit, live, bits, cnt + wv * BINS, rank, rounds);
+        __syncthreads();
+        digit_places<SMALL_WAVES>(cnt, bins, tot, wsum);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (live[r]) buf[tot[digit[r]] + cnt[wv * BINS + digit[r]] + rank[r]] = item[r];
+        __syncthreads();
+    }
+}
+
 // Up to SMALL_T tokens: workgroup k < parts sorts the ids of the k-th range of `range` ids;
 // the others fill zeros.  A sorting workgroup reads every id: it counts those below its
 // range, which gives the place of its output without a word from the others, and takes its
 // own, in order, into LDS (all of them, if all are in one range), as (id - first of the
-// range, position) in one word with `pos_bits` low bits of position.
+// range, position) in one word with `pos_bits` low bits of position.  The code runs once,
+// so its length counts: a workgroup enters the form of the sort that its items need.
 __global__ __launch_bounds__(1024) void sort_small_kernel(const void* ids, int id64, int64_t vocab, int tokens,
                                                           int parts, uint32_t range, int passes, int bits,
                                                           int pos_bits, uint32_t* skey, uint32_t* spos, Fill fill) {
@@ -181,39 +211,27 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(const void* ids, int i
         return;
     }
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
-    const int bins = 1 << bits;
     const uint32_t lo = blockIdx.x * range;
-    uint32_t item[16], digit[16], rank[16];
-    bool live[16];
-    int rounds = (tokens + 1023) / 1024;
+    const int rounds = (tokens + 1023) / 1024;
     // item number (wave, round, lane): each wave a contiguous piece; every load is issued
-    // before the first is looked at, so none is under a condition
+    // before the first is looked at (clamped, so that none is under a condition)
+    const int first = wv * rounds * 64 + lane;
+    uint32_t key[16], mine = 0, below = 0;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const int i = (wv * rounds + r) * 64 + lane;
-        live[r] = r < rounds && i < tokens;
-        item[r] = key_at(ids, id64, vocab, min(i, tokens - 1));
-    }
-    uint32_t mine = 0, below = 0;
+    for (int r = 0; r < 16; ++r) key[r] = key_at(ids, id64, vocab, min(first + r * 64, tokens - 1));
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        if (r >= rounds) {
-            live[r] = false;
-            continue;
+    for (int r = 0; r < 16; ++r)
+        if (r < rounds) {
+            const bool have = first + r * 64 < tokens;
+            below += __popcll(__ballot(have && key[r] < lo));
+            mine += __popcll(__ballot(have && key[r] - lo < range));     // below: wraps to a large number
         }
-        below += __popcll(__ballot(live[r] && item[r] < lo));
-        live[r] = live[r] && item[r] - lo < range;           // below: wraps to a large number
-        const uint64_t m = __ballot(live[r]);
-        rank[r] = mine + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u));
-        mine += __popcll(m);
-    }
     if (lane == 0) {
         wsum[wv] = mine;
         wbelow[wv] = below;
     }
     __syncthreads();
     uint32_t at = 0, n = 0, out = 0;
-#pragma unroll
     for (int w = 0; w < SMALL_WAVES; ++w) {
         const uint32_t c = wsum[w];
         at += w < wv ? c : 0u;
@@ -222,27 +240,21 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(const void* ids, int i
     }
 #pragma unroll
     for (int r = 0; r < 16; ++r)
-        if (live[r]) buf[at + rank[r]] = (item[r] - lo) << pos_bits | (uint32_t)((wv * rounds + r) * 64 + lane);
-    rounds = ((int)n + 1023) / 1024;
-    for (int p = 0; p < passes; ++p) {
-        for (int i = lane; i < bins; i += 64) cnt[wv * BINS + i] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int i = (wv * rounds + r) * 64 + lane;
-            live[r] = r < rounds && i < (int)n;
-            if (r >= rounds) continue;
-            item[r] = buf[min(i, SMALL_T - 1)];
-            digit[r] = (item[r] >> (pos_bits + p * bits)) & (uint32_t)(bins - 1);
+        if (r < rounds) {
+            const bool take = first + r * 64 < tokens && key[r] - lo < range;
+            const uint64_t m = __ballot(take);
+            if (take)
+                buf[at + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0u))] =
+                    (key[r] - lo) << pos_bits | (uint32_t)(first + r * 64);
+            at += __popcll(m);
         }
-        wave_ranks<16>(digit, live, bits, cnt + wv * BINS, rank, rounds);
-        __syncthreads();
-        digit_places<SMALL_WAVES>(cnt, bins, tot, wsum);
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-            if (live[r]) buf[tot[digit[r]] + cnt[wv * BINS + digit[r]] + rank[r]] = item[r];
-        __syncthreads();
-    }
+    // the first pass's barrier comes before any item is read
+    if (n <= 1024)
+        sort_in_lds<1>(buf, (int)n, pos_bits, passes, bits, cnt, tot, wsum);
+    else if (n <= 4096)
+        sort_in_lds<4>(buf, (int)n, pos_bits, passes, bits, cnt, tot, wsum);
+    else
+        sort_in_lds<16>(buf, (int)n, pos_bits, passes, bits, cnt, tot, wsum);
     for (int i = tid; i < (int)n; i += 1024) {
         stg(skey + out + i, lo + (buf[i] >> pos_bits));
         stg(spos + out + i, buf[i] & ((1u << pos_bits) - 1));
@@ -375,35 +387,93 @@ __device__ __forceinline__ typename Vec8<T>::Raw load_cols(const T* row, const C
     return k.whole ? load8(row + (k.n ? k.c : 0)) : load8_edge(row, k.c, k.dim);
 }
 
-// Sums of a chunk's runs, BATCH positions in flight at a time; with ACC the rows of G that a
-// run is added to are loaded beside them, for every position (those of one run are one row).
-template <class T, bool ACC, int BATCH>
-__device__ __forceinline__ void run_sums(const RunSum& s, const Cols& cols, uint32_t chunk, uint32_t k, uint32_t p) {
-    const uint32_t prev = (uint32_t)__builtin_amdgcn_readlane((int)k, CHUNK);
-    const uint32_t next = (uint32_t)__builtin_amdgcn_readlane((int)k, CHUNK + 1);
-    floatx8 acc = {};
-    bool begun_before = (uint32_t)__builtin_amdgcn_readlane((int)k, 0) == prev;
+// One wave per sorted position and 512 columns; it has work where a run of equal ids begins, or
+// a chunk does inside one, and sums the run's tokens up to the chunk's end.
+template <class T, bool ACC>
+__global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
+    const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t i = wave / s.col_tiles;
+    if (i >= s.tokens) return;
+    const int lane = threadIdx.x & 63;
+    // lane l holds sorted position i - 1 + l (the ends again beyond the list)
+    const int64_t in = min(max(i - 1 + lane, (int64_t)0), s.tokens - 1);
+    const uint32_t k = ldg(s.key + in), p = ldg(s.pos + in);
+    const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, 1);
+    if (key >= s.vocab) return;                              // tokens without a row come last
+    const int begin = (int)(i % CHUNK);
+    const uint64_t same = __ballot(k == key && i - 1 + lane < s.tokens);
+    const bool begun_before = i > 0 && (same & 1);
+    if (begun_before && begin != 0) return;
+    const int run = __builtin_ctzll(~(same >> 1));           // 63 at most: more than a chunk
+    const int count = min(run, CHUNK - begin);
+    const bool goes_on = run > count;
+    const Cols cols = lane_cols(wave - (uint32_t)i * s.col_tiles, s.dim);
+    const auto row = [&](int j) {
+        const T* d = (const T*)s.dout + (int64_t)(uint32_t)__builtin_amdgcn_readlane((int)p, 1 + j) * s.lddout;
+        return load_cols(d, cols);
+    };
+    const bool whole_run = !begun_before && !goes_on;
+    float* g = s.g + (int64_t)key * s.ldg;
+    typename Vec8<float>::Raw old = {};
+    if (ACC && whole_run) old = load_cols((const float*)g, cols);
+    floatx8 acc = Vec8<T>::get(row(0));
+    for (int j = 1; j < count; j += 4) {
+        typename Vec8<T>::Raw r[4];
 #pragma unroll
-    for (int b = 0; b < CHUNK; b += BATCH) {
-        typename Vec8<T>::Raw r[BATCH];
-        typename Vec8<float>::Raw g[ACC ? BATCH : 1];
+        for (int q = 0; q < 4; ++q) r[q] = row(min(j + q, count - 1));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (j + q < count) acc += Vec8<T>::get(r[q]);
+    }
+    if (cols.n == 0) return;
+    if (whole_run) {
+        acc *= s.scale;
+        if constexpr (ACC) acc += Vec8<float>::get(old);
+        store8_n(g + cols.c, Vec8<float>::put(acc), cols.n);
+    } else {
+        store8((begun_before ? s.first : s.last) + i / CHUNK * s.pitch + cols.c, Vec8<float>::put(acc));
+    }
+}
+
+constexpr int BATCH = 4;                     // positions processed while the next are on their way
+
+// The same by one wave per chunk and 512 columns, for long lists.  With ACC the rows of G that a run is added to are loaded beside its
+// tokens', for every position (those of one run are one row).  WHOLE: Cols::whole.
+template <class T, bool ACC, bool WHOLE>
+__device__ __forceinline__ void chunk_sums(const RunSum& s, const Cols& cols, uint32_t chunk, uint32_t k, uint32_t p) {
+    using Raw = typename Vec8<T>::Raw;
+    using RawG = typename Vec8<float>::Raw;
+    const int64_t c = WHOLE && cols.n == 0 ? 0 : cols.c;
+    const auto load = [&](Raw (&r)[BATCH], RawG (&g)[BATCH], int b) {
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             // positions past the end and tokens without a row load a row that exists
             const uint32_t row = (uint32_t)__builtin_amdgcn_readlane((int)p, b + i);
-            r[i] = load_cols((const T*)s.dout + (int64_t)row * s.lddout, cols);
+            const T* d = (const T*)s.dout + (int64_t)row * s.lddout;
+            r[i] = WHOLE ? load8(d + c) : load8_edge(d, c, s.dim);
             if constexpr (ACC) {
                 const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
-                g[i] = load_cols((const float*)s.g + (int64_t)(key < s.vocab ? key : 0) * s.ldg, cols);
+                const float* e = s.g + (int64_t)(key < s.vocab ? key : 0) * s.ldg;
+                g[i] = WHOLE ? load8(e + c) : load8_edge(e, c, s.dim);
             }
         }
+    };
+    floatx8 acc = {};
+    // the key before the chunk is on lane CHUNK, the one after it on lane CHUNK + 1
+    bool begun_before = __builtin_amdgcn_readlane((int)k, 0) == __builtin_amdgcn_readlane((int)k, CHUNK);
+    Raw r[BATCH], r2[BATCH];
+    RawG g[BATCH], g2[BATCH];
+    load(r, g, 0);
+#pragma unroll 1
+    for (int b = 0; b < CHUNK; b += BATCH) {
+        load(r2, g2, b + BATCH < CHUNK ? b + BATCH : b);
 #pragma unroll
         for (int i = 0; i < BATCH; ++i) {
             const uint32_t key = (uint32_t)__builtin_amdgcn_readlane((int)k, b + i);
             if (key >= s.vocab) return;        // tokens without a row come last
-            const uint32_t after = b + i + 1 < CHUNK ? (uint32_t)__builtin_amdgcn_readlane((int)k, (b + i + 1) % 64) : next;
-            acc += Vec8<T>::get(r[i]);
             const bool at_end = b + i + 1 == CHUNK;
+            const uint32_t after = (uint32_t)__builtin_amdgcn_readlane((int)k, at_end ? CHUNK + 1 : b + i + 1);
+            acc += Vec8<T>::get(r[i]);
             if (key != after || at_end) {
                 const bool goes_on = at_end && key == after;
                 if (begun_before || goes_on) {
@@ -412,17 +482,26 @@ __device__ __forceinline__ void run_sums(const RunSum& s, const Cols& cols, uint
                 } else {
                     floatx8 v = acc * s.scale;
                     if constexpr (ACC) v += Vec8<float>::get(g[i]);
-                    store8_n(s.g + (int64_t)key * s.ldg + cols.c, Vec8<float>::put(v), cols.n);
+                    float* row = s.g + (int64_t)key * s.ldg + cols.c;
+                    if (!WHOLE)
+                        store8_n(row, Vec8<float>::put(v), cols.n);
+                    else if (cols.n > 0)
+                        store8(row, Vec8<float>::put(v));
                 }
                 acc = floatx8{};
                 begun_before = false;
             }
         }
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            r[i] = r2[i];
+            g[i] = g2[i];
+        }
     }
 }
 
 template <class T, bool ACC>
-__global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
+__global__ __launch_bounds__(256) void chunk_sums_kernel(RunSum s) {
     const uint32_t wave = blockIdx.x * 4 + (threadIdx.x >> 6);
     const uint32_t chunk = wave / s.col_tiles;
     if (chunk >= s.chunks) return;
@@ -431,14 +510,15 @@ __global__ __launch_bounds__(256) void run_sums_kernel(RunSum s) {
     const int64_t i0 = (int64_t)chunk * CHUNK;
     const int count = (int)min((int64_t)CHUNK, s.tokens - i0);
     // lane i < CHUNK holds position i0 + i; lanes CHUNK and CHUNK + 1 the keys on either side
-    uint32_t k = 0xffffffffu, p = 0;
     const int64_t at = lane < CHUNK ? i0 + lane : lane == CHUNK ? i0 - 1 : i0 + CHUNK;
     const bool have = (lane < count || lane >= CHUNK) && lane <= CHUNK + 1 && at >= 0 && at < s.tokens;
-    if (have) {
-        k = ldg(s.key + at);
-        p = ldg(s.pos + at);
-    }
-    run_sums<T, ACC, ACC ? CHUNK / 2 : CHUNK>(s, cols, chunk, k, p);
+    const int64_t in = min(max(at, (int64_t)0), s.tokens - 1);
+    uint32_t k = ldg(s.key + in), p = ldg(s.pos + in);
+    if (!have) k = 0xffffffffu;
+    if (cols.whole)
+        chunk_sums<T, ACC, true>(s, cols, chunk, k, p);
+    else
+        chunk_sums<T, ACC, false>(s, cols, chunk, k, p);
 }
 
 // Partial rows from, from + step, .. up to `end` of the run that begins in `chunk`, in order,
@@ -524,12 +604,23 @@ __global__ __launch_bounds__(64 * JOIN_WAVES) void join_runs_kernel(RunSum s) {
 }
 
 template <class T>
-void run_sums_of(const RunSum& r, uint32_t waves, hipStream_t stream) {
-    const dim3 grid((waves + 3) / 4);
-    if (r.accumulate)
-        S4_LAUNCH((run_sums_kernel<T, true>), grid, dim3(256), 0, stream, r);
-    else
-        S4_LAUNCH((run_sums_kernel<T, false>), grid, dim3(256), 0, stream, r);
+void run_sums_of(const RunSum& r, hipStream_t stream) {
+    // A wave per position while all of them are resident at once (eight a SIMD), else a wave
+    // per chunk.  Measured, position against chunk: 1000 x 577 fp32 added 6.9 and 15.6 us,
+    // 1000 x 1024 bf16 7.2 and 8.1, 4000 x 1024 bf16 9.5 and 8.3, 16384 x 1024 bf16 31 and 20.
+    if (r.tokens * r.col_tiles <= 8192) {
+        const dim3 grid((uint32_t)((r.tokens * r.col_tiles + 3) / 4));
+        if (r.accumulate)
+            S4_LAUNCH((run_sums_kernel<T, true>), grid, dim3(256), 0, stream, r);
+        else
+            S4_LAUNCH((run_sums_kernel<T, false>), grid, dim3(256), 0, stream, r);
+    } else {
+        const dim3 grid((r.chunks * r.col_tiles + 3) / 4);
+        if (r.accumulate)
+            S4_LAUNCH((chunk_sums_kernel<T, true>), grid, dim3(256), 0, stream, r);
+        else
+            S4_LAUNCH((chunk_sums_kernel<T, false>), grid, dim3(256), 0, stream, r);
+    }
 }
 
 struct GradPlan {
@@ -594,10 +685,14 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
     const GradPlan p = grad_plan(e.tokens, e.vocab, e.dim);
     char* ws = (char*)workspace;
     Fill fill{e.accumulate ? nullptr : e.g, e.vocab, e.dim, e.ldg, 0, 1};
-    // workgroups that fill: 8 KB a workgroup and turn, at most four a CU
+    // workgroups that fill, 16 KB a turn each: a whole number, up to `each`, for every CU that
+    // the sort leaves free (in the small sort its LDS lets one run on a CU at a time, so a
+    // remainder would cost a whole turn of them: 46 us against 40 at 65536 x 1024)
     const int64_t fill_bytes = e.accumulate ? 0 : e.vocab * e.dim * 4;
-    const auto fill_blocks = [&](int parts) {
-        return (uint32_t)std::min<int64_t>(1024, (fill_bytes / parts + 8191) / 8192);
+    const auto fill_blocks = [&](int64_t sorters, int launches, int each) {
+        const int64_t cus = std::max<int64_t>(64, 256 - sorters);
+        const int64_t turns = (fill_bytes / launches + 16383) / 16384;
+        return (uint32_t)std::min(turns, std::min<int64_t>(each, (turns + cus - 1) / cus) * cus);
     };
     uint32_t *skey, *spos;
     if (e.tokens == 0 && fill_bytes == 0) return hipSuccess;
@@ -605,11 +700,11 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
         skey = (uint32_t*)(ws + p.off_key[0]);
         spos = (uint32_t*)(ws + p.off_pos[0]);
         const int parts = e.tokens == 0 ? 0 : p.parts;       // no tokens: nothing is read
-        S4_LAUNCH(sort_small_kernel, dim3(parts + fill_blocks(1)), dim3(1024), 0, stream, e.ids, e.id64, e.vocab,
+        S4_LAUNCH(sort_small_kernel, dim3(parts + fill_blocks(parts, 1, 4)), dim3(1024), 0, stream, e.ids, e.id64, e.vocab,
                   (int)e.tokens, parts, p.range, p.passes, p.digit, p.pos_bits, skey, spos, fill);
     } else {
         fill.parts = 2 * p.passes;
-        const uint32_t nf = fill_blocks(fill.parts);
+        const uint32_t nf = fill_blocks(p.nblk, fill.parts, 4);
         for (int k = 0; k < p.passes; ++k) {
             SortPass s;
             s.ids = k == 0 ? e.ids : nullptr;
@@ -652,9 +747,9 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
     r.accumulate = e.accumulate;
     const uint32_t waves = r.chunks * r.col_tiles;
     switch (dtype) {
-        case SHAMPOO4_BF16: run_sums_of<__bf16>(r, waves, stream); break;
-        case SHAMPOO4_F16: run_sums_of<_Float16>(r, waves, stream); break;
-        default: run_sums_of<float>(r, waves, stream);
+        case SHAMPOO4_BF16: run_sums_of<__bf16>(r, stream); break;
+        case SHAMPOO4_F16: run_sums_of<_Float16>(r, stream); break;
+        default: run_sums_of<float>(r, stream);
     }
     if (r.chunks > 1)
         S4_LAUNCH(join_runs_kernel, dim3((waves + JOIN_WAVES - 1) / JOIN_WAVES), dim3(64 * JOIN_WAVES), 0, stream, r);

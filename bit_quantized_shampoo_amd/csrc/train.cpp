@@ -63,8 +63,8 @@ bool wgrad_shape_ok(int64_t rows, int64_t n, int64_t cols) {
 
 bool embed_shape_ok(int64_t tokens, int64_t vocab, int64_t dim) {
     if (tokens < 0 || vocab < 1 || dim < 1 || tokens > kMaxDim || vocab > kMaxDim || dim > kMaxDim) return false;
-    // chunks of 16 tokens x tiles of 512 columns, 512 threads each in a launch
-    return (tokens + 15) / 16 * ((dim + 511) / 512) < (int64_t(1) << 23);
+    // chunks of 16 tokens x tiles of 512 columns, 64 threads each in a launch
+    return (tokens + 15) / 16 * ((dim + 511) / 512) < (int64_t(1) << 26) - 8;
 }
 
 bool policy_shape_ok(int64_t rows, int64_t vocab) {

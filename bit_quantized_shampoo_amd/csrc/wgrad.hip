@@ -350,8 +350,9 @@ struct WPlan {
 // and reading their partial sums (5 bytes a ns, and 2000 ns for the launch that joins them):
 // 16384 x 1024 x 4096 takes 142 us in four ranges of 64 large tiles, 182 us in 256 small
 // tiles and 351 us in 64 large ones; 2048 x 2048 x 2048 28 us in 256 small tiles, 44 us in
-// four ranges of 64 large ones.  A range has at least 128 tokens.
-WPlan wgrad_plan(int64_t rows, int64_t n, int64_t cols) {
+// four ranges of 64 large ones.  A range has at least 128 tokens.  An f16 or f32 dY is two or
+// three products an element.
+WPlan wgrad_plan(int64_t rows, int64_t n, int64_t cols, int pieces) {
     WPlan best{};
     double best_ns = 0;
     for (int k = 0; k < 2; ++k) {
@@ -365,7 +366,7 @@ WPlan wgrad_plan(int64_t rows, int64_t n, int64_t cols) {
             p.rows_per = ((rows + s - 1) / s + 63) / 64 * 64;
             p.splits = rows > 0 ? (int)((rows + p.rows_per - 1) / p.rows_per) : 1;
             if (p.splits != s) continue;
-            double ns = (double)((tiles * s + 255) / 256) * (double)p.rows_per * (p.large ? 28. : 11.);
+            double ns = (double)((tiles * s + 255) / 256) * (double)p.rows_per * pieces * (p.large ? 28. : 11.);
             if (s > 1) ns += 2000. + (2. * s + 1) * (double)(n * cols) * 4 / 5e3;
             if (best.splits == 0 || ns < best_ns) {
                 best = p;
@@ -397,13 +398,19 @@ hipError_t wgrad_of(const WGrad& w, const WPlan& p, hipStream_t stream) {
 }  // namespace
 
 size_t wgrad_workspace_bytes(int64_t rows, int64_t n, int64_t cols) {
-    const WPlan p = wgrad_plan(rows, n, cols);
-    return p.splits > 1 ? (size_t)p.splits * n * cols * 4 : 0;
+    // the most that any type's plan takes
+    size_t most = 0;
+    for (int pieces = 1; pieces <= 3; ++pieces) {
+        const WPlan p = wgrad_plan(rows, n, cols, pieces);
+        if (p.splits > 1) most = std::max(most, (size_t)p.splits * n * cols * 4);
+    }
+    return most;
 }
 
 hipError_t launch_wgrad(shampoo4_dtype dtype, const WGrad& w, hipStream_t stream) {
     if (w.n <= 0 || w.cols <= 0) return hipSuccess;
-    const WPlan p = wgrad_plan(w.rows, w.n, w.cols);
+    const int pieces = dtype == SHAMPOO4_BF16 ? 1 : dtype == SHAMPOO4_F16 ? 2 : 3;
+    const WPlan p = wgrad_plan(w.rows, w.n, w.cols, pieces);
     const bool part = p.splits > 1;
     hipError_t e;
     switch (dtype) {
