@@ -82,23 +82,45 @@ __device__ __forceinline__ void store_row(T* p, int64_t ld, int i, typename Vec8
         store8_n(p + i * ld, v, t.ncol);
 }
 
+typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
+
+// Larger magnitude bits: of one fp32 value, or of two 16-bit ones side by side.
+template <class T>
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 4) return max(a, b);
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(ushort2v, a), __builtin_bit_cast(ushort2v, b)));
+}
+
+// The largest over the lanes that hold the same columns (2 ROWS apart): rotations within
+// sixteen lanes, then exchanges of sixteen-lane rows and of halves, all without LDS.
+template <class T, int ROWS>
+__device__ __forceinline__ uint32_t over_groups(uint32_t m) {
+    if constexpr (ROWS == 2) {
+        m = larger<T>(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, false));    // row_ror:4
+        m = larger<T>(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xf, 0xf, false));    // row_ror:8
+    }
+    const auto h = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = larger<T>(h[0], h[1]);
+    const auto w = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return larger<T>(w[0], w[1]);
+}
+
 // Exponents of the lane's eight columns: maxima over its rows, then over the row groups.
 // Values are compared as bits, where NaN is above infinity.
 template <class T, int ROWS>
 __device__ __forceinline__ void exponents(const typename Vec8<T>::Raw (&r)[ROWS], uint32_t (&e)[8]) {
-    uint32_t m[8] = {};
+    constexpr int N = sizeof(r[0]) / 4;
+    constexpr uint32_t MAG = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
+    typename Vec8<T>::Raw m = {};
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-        const floatx8 f = Vec8<T>::get(r[i]);
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = max(m[j], __float_as_uint(f[j]) & 0x7fffffffu);
-    }
+        for (int j = 0; j < N; ++j) m[j] = larger<T>(m[j], r[i][j] & MAG);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < N; ++j) m[j] = over_groups<T, ROWS>(m[j]);
+    const floatx8 f = Vec8<T>::get(m);
 #pragma unroll
-        for (int o = 2 * ROWS; o < 64; o *= 2) m[j] = max(m[j], (uint32_t)__shfl_xor((int)m[j], o));
-        e[j] = act8_exponent(m[j]);
-    }
+    for (int j = 0; j < 8; ++j) e[j] = act8_exponent(__float_as_uint(f[j]));
 }
 
 // Codes and exponents of a loaded tile.  Every lane inside the padded columns writes
