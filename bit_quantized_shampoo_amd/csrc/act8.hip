@@ -207,7 +207,8 @@ __device__ __forceinline__ float act_sigmoid(float x) {
 }
 template <int KIND>
 __device__ __forceinline__ float act_derivative(float x, float sg) {
-    const float dz = KIND == SHAMPOO4_ACT_SILU ? 1.f : 1.5957691216f * fmaf(0.134145f * x, x, 1.f);
+    // bounded where the sigmoid is 0 or 1 and the product below is 0, so that it stays 0
+    const float dz = KIND == SHAMPOO4_ACT_SILU ? 1.f : 1.5957691216f * fmaf(0.134145f, fminf(x * x, 1e8f), 1.f);
     return fmaf(x * sg * (1.f - sg), dz, sg);
 }
 

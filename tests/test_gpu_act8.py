@@ -311,3 +311,117 @@ def test_other_stream():
     y = act8_load(act8_store(x, stream=s), stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(y, want)
+
+
+def test_weight_grad_with_a_very_long_leading_dimension():
+    """A leading dimension of more than 2^24 elements, and rows more than 2^31 bytes apart in all."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_store, act8_weight_grad
+    t, n, c = 70, 130, 40
+    announce("weight gradient, leading dimension 2^24 + 8")
+    big = torch.zeros((t, (1 << 24) + 8), dtype=torch.bfloat16, device="cuda")
+    dy = torch.randn(t, n, device="cuda").bfloat16()
+    big[:, 5:5 + n] = dy
+    x8 = act8_store(torch.randn(t, c, device="cuda"))
+    assert torch.equal(act8_weight_grad(big[:, 5:5 + n], x8), act8_weight_grad(dy, x8))
+
+
+def test_weight_grad_ignores_what_lies_between_rows():
+    """NaN in the padding of dY's rows, and in what follows its last row, changes nothing."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_store, act8_weight_grad
+    for t, n, c in ((300, 130, 200), (64, 300, 270)):
+        for dt in (torch.bfloat16, torch.float32):
+            dy = torch.randn(t, n, device="cuda").to(dt)
+            big = torch.full((t + 9, n + 37), float("nan"), dtype=dt, device="cuda")
+            big[:t, :n] = dy
+            x8 = act8_store(torch.randn(t, c, device="cuda"))
+            announce(f"weight gradient between rows {t}x{n}x{c} {dt}")
+            assert torch.equal(act8_weight_grad(big[:t, :n], x8), act8_weight_grad(dy, x8))
+
+
+def test_binding_refusals():
+    require_gpu()
+    import bit_quantized_shampoo_amd as s4
+    x = torch.randn(64, 48, device="cuda")
+    x8 = s4.act8_store(x)
+    bad = [
+        (ValueError, lambda: s4.act8_store(x.t())),                                  # column-major
+        (ValueError, lambda: s4.act8_store(x[:, ::2])),
+        (ValueError, lambda: s4.act8_store(x[:1].expand(64, 48))),                   # broadcast rows
+        (ValueError, lambda: s4.act8_store(x[0])),
+        (ValueError, lambda: s4.act8_store(x[:, :0])),
+        (TypeError, lambda: s4.act8_store(x.double())),
+        (ValueError, lambda: s4.act8_store(x[:32], out=x8)),
+        (ValueError, lambda: s4.Act8(x8.codes, x8.scales, 64, 49)),
+        (ValueError, lambda: s4.Act8(x8.codes.view(torch.uint8), x8.scales, 64, 48)),
+        (TypeError, lambda: s4.act8_load(x8, dtype=torch.int8)),
+        (ValueError, lambda: s4.act8_load(x8, out=x[:63])),
+        (ValueError, lambda: s4.activation_forward(x, x[:32])),
+        (TypeError, lambda: s4.activation_forward(x, x.bfloat16())),
+        (ValueError, lambda: s4.activation_backward(x[:32], x8)),
+        (ValueError, lambda: s4.activation_backward(x, x8, dup=x)),
+        (TypeError, lambda: s4.act8_weight_grad(x, x)),
+        (ValueError, lambda: s4.act8_weight_grad(x[:32], x8)),
+        (ValueError, lambda: s4.act8_weight_grad(x, x8, beta=1.0)),
+        (TypeError, lambda: s4.act8_weight_grad(x, x8, out=torch.zeros(48, 48, device="cuda").bfloat16())),
+        (ValueError, lambda: s4.embedding(x, torch.zeros(2, 2, dtype=torch.int64, device="cuda"))),
+        (TypeError, lambda: s4.embedding(x, torch.zeros(2, device="cuda"))),
+        (ValueError, lambda: s4.embedding_grad(x, torch.zeros(3, dtype=torch.int64, device="cuda"), 5)),
+        (ValueError, lambda: s4.embedding_grad(x, torch.zeros(64, dtype=torch.int64, device="cuda"), 5, accumulate=True)),
+        (ValueError, lambda: s4.embedding_grad(x, torch.zeros(64, dtype=torch.int64, device="cuda"), 5,
+                                               workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))),
+        (ValueError, lambda: s4.token_logprobs(x, torch.zeros(63, dtype=torch.int64, device="cuda"))),
+        (ValueError, lambda: s4.policy_loss(x, torch.zeros(64, dtype=torch.int64, device="cuda"), x[:, 0].contiguous(),
+                                            x[:, 0].contiguous(), x[:, 0].contiguous(), kl_coef=0.1)),
+        (ValueError, lambda: s4.policy_loss(x, torch.zeros(64, dtype=torch.int64, device="cuda"), x[:, 0],
+                                            x[:, 0].contiguous(), x[:, 0].contiguous())),
+        (s4.Shampoo4Error, lambda: s4.policy_loss(x, torch.zeros(64, dtype=torch.int64, device="cuda"),
+                                                  *[x[:, 0].contiguous()] * 3, clip_low=-1.0)),
+    ]
+    for k, (error, call) in enumerate(bad):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"call {k} was not refused")
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activation_gradient_at_extremes(kind):
+    """Far from 0 the derivative is 0 or 1, also where the cube of the argument overflows."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_store, activation_backward
+    x = torch.tensor([[-1e30, -1e20, -1e10, -300.0, 300.0, 1e10, 1e20, 1e30]], device="cuda")
+    announce(f"activation gradient extremes {kind}")
+    dg, _ = activation_backward(torch.full_like(x, 2.0), act8_store(x), kind=kind)
+    assert torch.equal(dg.abs(), torch.tensor([[0.0] * 4 + [2.0] * 4], device="cuda"))
+
+
+def test_captured_graphs():
+    """Forward, backward and weight gradient (with row ranges to join) from a captured graph,
+    replayed with other work between the replays, against the eager results."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_load, act8_store, act8_weight_grad, activation_backward, activation_forward
+    g, u, dh = (torch.randn(2100, 300, device="cuda").bfloat16() for _ in range(3))
+
+    def call():
+        h, g8, u8, h8 = activation_forward(g, u)
+        dg, du = activation_backward(dh, g8, u8)
+        return h, dg, du, act8_weight_grad(dh, h8), act8_load(act8_store(h))
+
+    want = call()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    announce("activation and weight gradient graph")
+    with torch.cuda.stream(s):
+        call()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = call()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        torch.randn(1000, 1000, device="cuda").sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))

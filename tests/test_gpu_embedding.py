@@ -105,7 +105,7 @@ def test_grad(t, v, d, dt, how, accumulate):
 @pytest.mark.parametrize("t,v,d,dt,how,idt", [
     (16385, 511, 16, "f32", "zipf", torch.int32), (20000, 300000, 8, "bf16", "uniform", torch.int64),
     (40000, 65536, 8, "f32", "zipf", torch.int64), (30000, 2, 8, "f32", "few", torch.int32),
-    (9000, 1 << 20, 8, "bf16", "uniform", torch.int32),
+    (9000, 1 << 20, 8, "bf16", "uniform", torch.int32), (9000, 1 << 24, 1, "f32", "uniform", torch.int64),
 ])
 def test_grad_sorted_in_blocks(t, v, d, dt, how, idt):
     """More tokens, or wider ids, than one workgroup's sort takes."""
@@ -152,3 +152,32 @@ def test_lookup_and_gradient_beyond_32_bit_offsets():
     grad = embedding_grad(out, ids, v)
     assert bool((grad[v - 1] == 6).all()) and float(grad[v - 2].abs().sum()) == 0
     assert float(grad[: v - 1].abs().amax()) == 0
+
+
+def test_captured_graphs():
+    """Lookup and gradient (sorted at once, and in blocks) from captured graphs, replayed with
+    other work between the replays, against the eager results."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import embedding, embedding_grad
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    for t, v in ((3000, 700), (20000, 5000)):
+        table = torch.randn(v, 40, generator=gen, device="cuda").bfloat16()
+        ids = torch.randint(-3, v + 3, (t,), generator=gen, device="cuda")
+        call = lambda: (lambda o: (o, embedding_grad(o, ids, v, scale=0.5)))(embedding(table, ids, scale=2.0))  # noqa: E731
+        want = call()
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        announce(f"embedding graph {t} of {v}")
+        with torch.cuda.stream(s):
+            call()
+            s.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                got = call()
+        for _ in range(3):
+            for x in got:
+                x.zero_()
+            torch.randn(1000, 1000, device="cuda").sum().item()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -231,3 +231,21 @@ def test_deterministic_and_captured():
             graph.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 logits; only the last rows count."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import policy_loss
+    rows, vocab = 33000, 65600
+    announce("policy loss with 64-bit offsets")
+    z = torch.empty((rows, vocab), dtype=torch.bfloat16, device="cuda")
+    z[-70:] = torch.randn(70, vocab, device="cuda").bfloat16()
+    y = torch.randint(0, vocab, (rows,), device="cuda")
+    old, adv, w = torch.full((rows,), -11.0, device="cuda"), torch.randn(rows, device="cuda"), torch.zeros(rows, device="cuda")
+    w[-70:] = 1.0
+    want = policy_loss(z[-70:].clone(), y[-70:], old[-70:], adv[-70:], w[-70:])
+    loss, logp, dz = policy_loss(z, y, old, adv, w, dlogits=z)
+    assert torch.equal(dz[-70:], want[2]) and torch.equal(logp[-70:], want[1])
+    assert abs(float(loss) - float(want[0])) <= 1e-5 * float(adv[-70:].abs().sum())
+    assert bool((dz[-71] == 0).all()) and bool((dz[0] == 0).all()) and float(logp[:-70].abs().sum()) == 0
