@@ -198,12 +198,24 @@ __global__ __launch_bounds__(256) void act8_load_kernel(Act8Ptr in, T* __restric
 
 // a(x) and a'(x) = sg + x sg (1 - sg) z'(x) with sg = 1 / (1 + exp(-z)): z = x (SiLU) or
 // 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU, tanh form).  No difference of near values, so
-// small and large arguments keep their relative precision.  The hardware exp2 and reciprocal
-// (1 ulp each) do: the argument's own rounding, |z| 2^-24 of the result, is larger.
+// small and large arguments keep their relative precision.  The hardware's exp2 and
+// reciprocal are good to an ulp; what would cost more is the rounding of the argument
+// -z log2 e, |z| 2^-24 of the result, so its remainder is kept and applied, and the
+// reciprocal takes one Newton step.  Past 100 on either side the sigmoid is 0 or 1 in fp32; a
+// NaN comes back with the product by x.
 template <int KIND>
 __device__ __forceinline__ float act_sigmoid(float x) {
-    const float z = KIND == SHAMPOO4_ACT_SILU ? x : 1.5957691216f * fmaf(0.044715f * x * x, x, x);
-    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950409f * z));
+    float z = KIND == SHAMPOO4_ACT_SILU ? x : 1.5957691216f * fmaf(0.044715f * x * x, x, x);
+    z = __builtin_amdgcn_fmed3f(z, -100.f, 100.f);
+    constexpr float HI = -1.44269502162933349609375f, LO = -1.925963033500e-8f;      // -log2 e
+    const float t = z * HI;
+    const float rest = fmaf(z, LO, fmaf(z, HI, -t));
+    float e = __builtin_amdgcn_exp2f(t);
+    e = fmaf(e * 0.693147180559945f, rest, e);
+    const float d = 1.f + e;
+    float y = __builtin_amdgcn_rcpf(d);
+    y = fmaf(fmaf(-d, y, 1.f), y, y);
+    return t > 126.f ? 0.f : y;
 }
 template <int KIND>
 __device__ __forceinline__ float act_derivative(float x, float sg) {

@@ -184,8 +184,9 @@ struct Act8Block {
         uint32_t b[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            // the clamp also turns a NaN into a number (fmaxf returns its other operand)
-            const float y = fminf(fmaxf(x[j] * inv[j], -top[j]), top[j]);
+            // the clamp also turns a NaN, in a block with top = 0, into 0 (of the median's
+            // operands a NaN is left out)
+            const float y = __builtin_amdgcn_fmed3f(x[j] * inv[j], -top[j], top[j]);
             b[j] = __float_as_uint(y + 12582912.f);
         }
         u32x2 r;
