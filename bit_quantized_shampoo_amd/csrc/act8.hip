@@ -2,15 +2,24 @@
 //
 // Format: shampoo4_train.h (blocks of 32 rows x 1 column, scale a power of two, codes in
 // two's complement).  All four kernels are HBM streams over the same tiles: a wave takes
-// 32 rows x 16 ROWS columns, each lane ROWS rows of eight columns (16 bytes in 16 bits).  A lane's row loads are
-// independent and all in flight at once; a block's maximum is ROWS maxima in registers and
-// butterflies over the row groups, so a block's rows are read once and nothing goes through
-// LDS.
+// 32 rows x 16 ROWS columns, each lane ROWS rows of eight columns (16 bytes in 16 bits).  A
+// lane's row loads are independent and all in flight at once; a block's maximum is ROWS
+// maxima in registers, as packed magnitudes, and three cross-lane steps over the row groups,
+// so a block's rows are read once and nothing goes through LDS.
+//
+// Large shapes are bound by HBM: [16384, 4096] bf16 stored in 39.4 us (5.2 TB/s) and loaded
+// in 31.6 (6.4 TB/s; part of the codes is still in the last-level cache); gated SiLU of
+// [8192, 4096] bf16 with both checkpoints in 61.1 us forward (4.4 TB/s) and 48.2 backward
+// (5.6 TB/s).  The counters show each
+// input read once and each output written once.  Small shapes take one launch and one trip
+// to memory: [16, 1024] bf16 3.1 us stored, 2.6 loaded.
 //
 // ROWS is 8, or 2 while the wide tiles are fewer than one a SIMD, where what counts is how
-// long a lane takes and not the 64-byte runs of its rows.  Measured with 8 and with 2 rows a
-// lane: gated SiLU forward of [16, 1021] bf16 11.9 and 5.9 us, of [1000, 2309] bf16 14.4 and
-// 10.0, of [2048, 4096] bf16 13.7 and 16.9, of [16384, 4096] bf16 80 and 109.
+// long a lane takes and not the 128-byte runs of a row.  Measured with 8 and with 2 rows a
+// lane: gated SiLU forward of [16, 1021] bf16 12.0 and 5.6 us, of [1000, 2309] bf16 14.8 and
+// 10.1, of [2048, 4096] bf16 15.6 and 19.2, of [16384, 4096] bf16 81 and 124.  Loading to
+// fp32 alone gains from 2 rows at every size (32 bytes a lane make long runs by themselves):
+// [4096, 4096] 18.9 and 17.7 us, [16384, 4096] 68 and 59.
 #include <type_traits>
 
 #include "train_common.hpp"
@@ -295,10 +304,9 @@ struct Cover {
     int64_t tiles;
     dim3 grid;
 };
-Cover cover(int64_t rows, int64_t cols) {
-    const int64_t wide = act8_tiles(rows, cols);
+Cover cover(int64_t rows, int64_t cols, bool narrow = false) {
     Cover c;
-    c.rows = wide >= 1024 ? 8 : 2;
+    c.rows = act8_tiles(rows, cols) >= 1024 && !narrow ? 8 : 2;
     c.tiles = (rows + 31) / 32 * ((cols + 16 * c.rows - 1) / (16 * c.rows));
     c.grid = dim3((uint32_t)((c.tiles + 3) / 4));
     return c;
@@ -337,11 +345,12 @@ hipError_t launch_act8_store(shampoo4_dtype dtype, int64_t rows, int64_t cols, c
 
 hipError_t launch_act8_load(shampoo4_dtype dtype, int64_t rows, int64_t cols, Act8Ptr in, void* x, int64_t ldx,
                             hipStream_t stream) {
-    const Cover c = cover(rows, cols);
+    const Cover c = cover(rows, cols, dtype == SHAMPOO4_F32);
     if (c.tiles <= 0) return hipSuccess;
     dispatch(dtype, c.rows, [&](auto t, auto r) {
         using T = decltype(t);
-        S4_LAUNCH((act8_load_kernel<T, decltype(r)::value>), c.grid, dim3(256), 0, stream, in, (T*)x, ldx, rows, cols,
+        constexpr int R = sizeof(T) == 4 ? 2 : decltype(r)::value;
+        S4_LAUNCH((act8_load_kernel<T, R>), c.grid, dim3(256), 0, stream, in, (T*)x, ldx, rows, cols,
                   c.tiles);
     });
     return hipGetLastError();

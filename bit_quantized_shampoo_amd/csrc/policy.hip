@@ -11,6 +11,12 @@
 //    ones: a launch of partial statistics over pieces of a row, and a launch that joins a
 //    row's pieces and writes its gradient piece by piece (the logits are read again).
 // The loss is summed in a fixed order: row terms by one workgroup at the end.
+//
+// Bound by HBM: 4096 rows of 65536 bf16 logits with their gradient in 195 us (5.5 TB/s for
+// 1.07 GB; a plain copy reaches 5.1), the loss's launch 4.9 more, behind it.  The counters
+// show every logit read once (and rows that do not count not at all) and every gradient
+// written once.  Few rows are bound by their two launches: 8 rows of 40961 fp32 logits 3.6
+// and 4.6 us.
 #include <algorithm>
 
 #include "train_common.hpp"

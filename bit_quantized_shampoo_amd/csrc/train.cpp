@@ -112,7 +112,9 @@ shampoo4_status shampoo4_act8_load(shampoo4_dtype dtype, int64_t rows, int64_t c
                                    const uint8_t* scales, void* x, int64_t ldx, void* stream) {
     CallRange range_("shampoo4_act8_load");
     if (!dtype_ok(dtype)) return SHAMPOO4_EINVAL;
-    if (!shape_ok(rows, cols) || act8_tiles(rows, cols) > ACT8_MAX_TILES) return SHAMPOO4_ESHAPE;
+    if (!shape_ok(rows, cols) ||
+        act8_tiles(rows, cols) > (dtype == SHAMPOO4_F32 ? ACT8_MAX_TILES_F32_LOAD : ACT8_MAX_TILES))
+        return SHAMPOO4_ESHAPE;
     S4_TRY(matrix_ok(x, dtype, rows, cols, ldx));
     S4_TRY(act8_ok(codes, scales, rows, true));
     return launched(launch_act8_load(dtype, rows, cols, {const_cast<int8_t*>(codes), const_cast<uint8_t*>(scales)}, x,

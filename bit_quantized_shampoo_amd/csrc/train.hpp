@@ -16,12 +16,15 @@ struct Act8Ptr {
 constexpr int64_t act8_rows(int64_t rows) { return (rows + 31) / 32 * 32; }
 constexpr int64_t act8_pitch(int64_t cols) { return (cols + 15) / 16 * 16; }
 
-// One wave covers ACT8_COLS columns of one block of 32 rows.
+// A wave's widest tile: ACT8_COLS columns of one block of 32 rows (the narrow one has a
+// quarter of them).
 constexpr int ACT8_COLS = 128;
 constexpr int64_t act8_tiles(int64_t rows, int64_t cols) {
     return (rows + 31) / 32 * ((cols + ACT8_COLS - 1) / ACT8_COLS);
 }
-constexpr int64_t ACT8_MAX_TILES = (int64_t(1) << 26) - 8;   // 64 threads each: below 2^32 in a launch
+// 64 threads a tile: below 2^32 in a launch.  Loading to fp32 always takes the narrow tiles.
+constexpr int64_t ACT8_MAX_TILES = (int64_t(1) << 26) - 8;
+constexpr int64_t ACT8_MAX_TILES_F32_LOAD = (int64_t(1) << 24) - 8;
 
 hipError_t launch_act8_store(shampoo4_dtype dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
                              Act8Ptr out, hipStream_t stream);

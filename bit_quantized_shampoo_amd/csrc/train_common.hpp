@@ -56,9 +56,6 @@ struct Vec8<float> {
 };
 
 template <class T>
-__device__ __forceinline__ float to_float(T v) { return (float)v; }
-
-template <class T>
 __device__ __forceinline__ typename Vec8<T>::Raw load8(const T* p) {
     using G = __attribute__((address_space(1))) const typename Vec8<T>::Mem;
     return *(G*)p;

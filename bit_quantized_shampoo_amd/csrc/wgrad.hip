@@ -3,10 +3,29 @@
 //
 // Both operands are contracted over their rows (tokens), so neither has consecutive
 // contraction elements in memory.  Tiles are staged in LDS as they lie in memory, token by
-// token, in bf16, and gfx950's transposing LDS read (four tokens of sixteen columns a group
-// of sixteen lanes) gives each lane the consecutive tokens that a matrix-core operand takes.
-// X^ = code * 2^k is a bf16 number exactly, and a bf16 dY is an operand as it stands; an f16
-// or f32 dY is split exactly into two or three bf16 pieces, one product each.
+// token, in bf16, and gfx950's transposing LDS read (four tokens of sixteen columns a group of
+// sixteen lanes) gives each lane the consecutive tokens that a matrix-core operand takes. X^ =
+// code * 2^k is a bf16 number exactly, and a bf16 dY is an operand as it stands; an f16 or f32
+// dY is split exactly into two or three bf16 pieces, one product each.
+//
+// Bound by the matrix cores.  A workgroup of eight waves holds 256 x 256 outputs in its
+// accumulators (128 a lane): the largest tile that two waves a SIMD leave registers for, so an
+// operand that is read from L2 once meets 256 others.  Slices of 64 tokens (32 where dY has
+// two or three pieces) alternate between two stages of LDS: while one is multiplied, the next
+// one's loads, conversion and LDS stores are spread over its products, and each unit's
+// operands are read from LDS while the unit before it is multiplied; one barrier a slice.  The
+// code bytes become bf16 here, five vector instructions a pair.
+//
+// 16384 x 4096 x 4096 bf16: 456-472 us, 1165-1205 TFLOP/s, where a library's plain bf16
+// product of these shapes (X^ in 16 bits) takes 446-460.  The matrix cores are busy for 63% of
+// the CUs' busy clocks, LDS reads take 40%, with no bank conflicts; the operands come through
+// L2 2.7 times.  With the staging left out the products and operand reads alone take 352 us,
+// so what remains is staging: its vector instructions and LDS stores take the issue slots
+// beside the products.  Measured and not better (all within 1%): more registers of loads in
+// flight, two units of operands ahead, wave priorities, one scale decoded for two rows, other
+// spreads of the staging over the units.  f32 dY 5461 x 4096 x 4096 430 us, f16 8192 x 4096 x
+// 4096 432, the same number of matrix-core products; 16384 x 1024 x 4096 bf16 136 us (library
+// 155), 8192 x 1024 x 1024 32 (52), 4096 x 4096 x 1024 48 (43).
 #include <algorithm>
 
 #include "train_common.hpp"
@@ -347,7 +366,7 @@ struct WPlan {
 // 28 ns a token on 256 x 256 tiles and 11 ns on 128 x 128 ones (bf16, measured where the
 // rounds are full: 16384 x 4096 x 4096 in 463 us against 663 us in four times the tiles).
 // Row ranges beyond one fill the GPU when the output alone cannot, at the cost of writing
-// and reading their partial sums (5 bytes a ns, and 2000 ns for the launch that joins them):
+// and reading their partial sums (5 TB/s, and 2000 ns for the launch that joins them):
 // 16384 x 1024 x 4096 takes 142 us in four ranges of 64 large tiles, 182 us in 256 small
 // tiles and 351 us in 64 large ones; 2048 x 2048 x 2048 28 us in 256 small tiles, 44 us in
 // four ranges of 64 large ones.  A range has at least 128 tokens.  An f16 or f32 dY is two or

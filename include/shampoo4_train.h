@@ -61,7 +61,9 @@ typedef enum {
 #define SHAMPOO4_ACT8_ROWS 32
 #define SHAMPOO4_ACT8_PITCH 16
 
-/* Bytes of codes and scales.  Host only.  ESHAPE: rows < 0, cols < 1, or above 2^31 - 64. */
+/* Bytes of codes and scales.  Host only.  ESHAPE: rows < 0, cols < 1, or above 2^31 - 64.
+ * The calls below refuse (ESHAPE) what one launch cannot cover: 2^26 tiles of 32 rows x 128
+ * columns, 2^24 where float32 values are loaded (both beyond this GPU's memory or near it). */
 SHAMPOO4_API shampoo4_status shampoo4_act8_bytes(int64_t rows, int64_t cols, size_t* codes_bytes,
                                                  size_t* scales_bytes);
 
@@ -107,7 +109,8 @@ SHAMPOO4_API shampoo4_status shampoo4_activation_backward(int32_t kind, shampoo4
  * are exact and sums in fp32 on the bf16 matrix cores: X^ and a bf16 dY are operands as
  * they stand, an f16 or f32 dY is split exactly into two or three bf16 pieces.
  * rows = 0: G = beta * G.  The workspace (NULL when the size is 0) holds partial sums of
- * row ranges when the output alone cannot fill the GPU. */
+ * row ranges when the output alone cannot fill the GPU.
+ * ESHAPE also from 2^23 output tiles of 64 x 64 on. */
 SHAMPOO4_API size_t shampoo4_act8_weight_grad_workspace_bytes(int64_t rows, int64_t n, int64_t cols);
 SHAMPOO4_API shampoo4_status shampoo4_act8_weight_grad(shampoo4_dtype dtype, int64_t rows, int64_t n, int64_t cols,
                                                        float alpha, const void* dy, int64_t lddy,
@@ -128,7 +131,8 @@ SHAMPOO4_API shampoo4_status shampoo4_embedding(shampoo4_dtype dtype, int32_t id
  * touches the rows of present tokens only.  Ids outside [0, vocab) contribute nothing.
  * The tokens are sorted by id (stable), so a row's sum is taken over its tokens in the
  * order of their positions, split at fixed places of the sorted list.
- * ESHAPE: tokens, vocab or dim above 2^31 - 64. */
+ * ESHAPE: tokens, vocab or dim above 2^31 - 64, or tokens / 16 * dim / 512 from 2^26 on (also
+ * of shampoo4_embedding). */
 SHAMPOO4_API size_t shampoo4_embedding_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t dim);
 SHAMPOO4_API shampoo4_status shampoo4_embedding_grad(shampoo4_dtype dtype, int32_t id_bytes, int64_t tokens,
                                                      int64_t vocab, int64_t dim, const void* dout, int64_t lddout,
@@ -149,7 +153,8 @@ SHAMPOO4_API shampoo4_status shampoo4_embedding_grad(shampoo4_dtype dtype, int32
  * A logit of -infinity has probability 0.
  * Outputs: loss, one fp32; logp, fp32 [rows], or NULL; dlogits [rows, vocab] of `dtype`, or
  * NULL for the loss alone (dlogits may be Z itself, with its leading dimension).  ref may
- * be NULL with kl_coef = 0 (it is then not read). */
+ * be NULL with kl_coef = 0 (it is then not read).
+ * ESHAPE: vocab < 1 or above 2^31 - 64, 2^22 rows or more, or rows * vocab / 32768 from 2^23 on. */
 typedef struct {
     float clip_low, clip_high;    /* >= 0; clip_low <= 1 */
     float kl_coef;                /* >= 0 */
