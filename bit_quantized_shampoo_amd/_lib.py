@@ -46,7 +46,8 @@ EXPORTED_TRAIN = [
     "shampoo4_act8_bytes", "shampoo4_act8_store", "shampoo4_act8_load", "shampoo4_activation_forward",
     "shampoo4_activation_backward", "shampoo4_act8_weight_grad_workspace_bytes", "shampoo4_act8_weight_grad",
     "shampoo4_embedding", "shampoo4_embedding_grad_workspace_bytes", "shampoo4_embedding_grad",
-    "shampoo4_policy_loss_workspace_bytes", "shampoo4_policy_loss", "shampoo4_token_logprobs",
+    "shampoo4_policy_loss_workspace_bytes", "shampoo4_policy_loss", "shampoo4_token_logprobs_workspace_bytes",
+    "shampoo4_token_logprobs",
 ]
 F32, BF16, F16 = 0, 1, 2
 ACT_SILU, ACT_GELU = 0, 1
@@ -168,6 +169,7 @@ def lib() -> ctypes.CDLL:
         "shampoo4_policy_loss_workspace_bytes": (sz, [i32, i64, i64]),
         "shampoo4_policy_loss": (st, [ctypes.POINTER(PolicyConfig), i32, i32, i64, i64, vp, i64, vp, vp, vp, vp, vp,
                                       vp, vp, vp, i64, vp, sz, vp]),
+        "shampoo4_token_logprobs_workspace_bytes": (sz, [i32, i64, i64]),
         "shampoo4_token_logprobs": (st, [i32, i32, i64, i64, vp, i64, vp, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():

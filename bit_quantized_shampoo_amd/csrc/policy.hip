@@ -378,8 +378,9 @@ __global__ __launch_bounds__(1024) void loss_sum_kernel(const float* __restrict_
 // Up to SPLIT_ROWS rows are split.  Measured (split launches against the row kernel and the
 // loss's): 8 x 32768 bf16 7.8 us against 11.4, 8 x 40961 fp32 7.9 against 12.2, 63 x 65536
 // bf16 11.7 against 14.6, 48 x 131072 bf16 11.2 against 19.9.  Shorter rows are a few
-// microseconds either way and take the row kernel; so do the log-probabilities alone up to
-// 32768 logits, one launch instead of two.
+// microseconds either way and take the row kernel; so do the log-probabilities alone, one
+// launch instead of two (a call among others: 16 x 65536 bf16 7.0 us against 10.7, 1 and 64 x
+// 131072 bf16 8.1 and 8.6 against 10.9 and 10.4).
 constexpr int64_t SPLIT_ROWS = 64;
 constexpr int64_t SPLIT_GROUPS = 1024;       // workgroups of a split launch, about
 
@@ -392,9 +393,9 @@ PolicyPlan policy_plan(shampoo4_dtype dtype, int64_t rows, int64_t vocab, bool t
     PolicyPlan q{};
     const int64_t nvec = vocab >> 3;
     const int64_t most = 1024 * (dtype == SHAMPOO4_F32 ? 8 : 16);    // vectors a workgroup holds
-    q.split = nvec > most || (rows <= SPLIT_ROWS && nvec > (train ? 1024 : 4096));
+    q.split = nvec > most || (train && rows <= SPLIT_ROWS && nvec > 1024);
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-    q.off_stat = up((size_t)rows * 4);
+    q.off_stat = up(train ? (size_t)rows * 4 : 0);
     q.total = q.off_stat;
     if (q.split) {
         const int64_t per_row = std::max<int64_t>(1, SPLIT_GROUPS / std::max<int64_t>(rows, 1));
@@ -442,8 +443,8 @@ bool policy_of(const Policy& p, const PolicyPlan& plan, char* ws, hipStream_t st
 
 }  // namespace
 
-size_t policy_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab) {
-    return policy_plan(dtype, rows, vocab, true).total;
+size_t policy_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab, bool train) {
+    return policy_plan(dtype, rows, vocab, train).total;
 }
 
 hipError_t launch_policy(shampoo4_dtype dtype, const Policy& p, void* workspace, hipStream_t stream) {

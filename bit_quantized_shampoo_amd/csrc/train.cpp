@@ -82,7 +82,7 @@ shampoo4_status policy_call(const Policy& p, shampoo4_dtype dtype, int32_t id_by
         if (!p.targets) return SHAMPOO4_EINVAL;
         if (!aligned(p.targets, id_bytes)) return SHAMPOO4_EALIGN;
     }
-    S4_TRY(workspace_ok(workspace, workspace_bytes, policy_workspace_bytes(dtype, p.rows, p.vocab)));
+    S4_TRY(workspace_ok(workspace, workspace_bytes, policy_workspace_bytes(dtype, p.rows, p.vocab, p.train != 0)));
     return launched(launch_policy(dtype, p, workspace, as_stream(stream)));
 }
 
@@ -215,7 +215,11 @@ shampoo4_status shampoo4_embedding_grad(shampoo4_dtype dtype, int32_t id_bytes, 
 }
 
 size_t shampoo4_policy_loss_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab) {
-    return dtype_ok(dtype) && policy_shape_ok(rows, vocab) ? policy_workspace_bytes(dtype, rows, vocab) : 0;
+    return dtype_ok(dtype) && policy_shape_ok(rows, vocab) ? policy_workspace_bytes(dtype, rows, vocab, true) : 0;
+}
+
+size_t shampoo4_token_logprobs_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab) {
+    return dtype_ok(dtype) && policy_shape_ok(rows, vocab) ? policy_workspace_bytes(dtype, rows, vocab, false) : 0;
 }
 
 shampoo4_status shampoo4_policy_loss(const shampoo4_policy_config* cfg, shampoo4_dtype dtype, int32_t id_bytes,

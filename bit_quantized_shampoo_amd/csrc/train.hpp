@@ -100,7 +100,7 @@ struct Policy {
     float clip_low, clip_high, kl, grad_scale;
     int id64, train;
 };
-size_t policy_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab);
+size_t policy_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab, bool train);
 hipError_t launch_policy(shampoo4_dtype dtype, const Policy& p, void* workspace, hipStream_t stream);
 
 }  // namespace s4

@@ -41,7 +41,7 @@ def _on_stream(fn):
 def _stream(device) -> int:
     """The current stream's handle; every tensor of a call is on `device`, the current one."""
     index = device.index
-    if index != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"tensors must be on the current device, got {device}")
     return torch._C._cuda_getCurrentRawStream(index)
 
@@ -82,10 +82,11 @@ def _matrix(t, what: str, dtype=None, rows=None, cols=None, device=None) -> int:
 
 
 def _vector(t, n: int, what: str, dtype, device):
-    _tensor(t, what)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _tensor(t, what)
     if t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.ndim != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous vector of {n}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
@@ -93,7 +94,8 @@ def _vector(t, n: int, what: str, dtype, device):
 
 
 def _ids(t, n: int, what: str, device) -> int:
-    _tensor(t, what)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        _tensor(t, what)
     if t.dtype not in _ID_BYTES:
         raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
     return _vector(t, n, what, t.dtype, device)
@@ -119,7 +121,9 @@ class Act8:
     uint8 [R / 32, P] (R: rows up to a multiple of 32, P: cols up to one of 16), the value
     of element (t, c) being codes[t, c] * 2 ** (scales[t // 32, c] - 127)."""
 
-    __slots__ = ("_codes", "_scales", "rows", "cols")
+    # Two tensors, or one buffer with the scales behind the codes (one allocation where a call
+    # makes the checkpoint), of which codes and scales are views made when asked for.
+    __slots__ = ("_buf", "_codes", "_scales", "rows", "cols")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int):
         r, p = self.padded(rows, cols)
@@ -129,10 +133,31 @@ class Act8:
                 raise ValueError(f"{nm} must be a contiguous {dtype} tensor of shape {want}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
-        self._codes, self._scales, self.rows, self.cols = codes, scales, rows, cols
+        self._buf, self._codes, self._scales, self.rows, self.cols = None, codes, scales, rows, cols
 
-    codes = property(lambda self: self._codes)
-    scales = property(lambda self: self._scales)
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            r, p = self.padded(self.rows, self.cols)
+            self._codes = self._buf[:r * p].view(_I8).view(r, p)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            r, p = self.padded(self.rows, self.cols)
+            self._scales = self._buf[r * p:].view(r // L.ACT8_ROWS, p)
+        return self._scales
+
+    @property
+    def device(self) -> torch.device:
+        return (self._codes if self._buf is None else self._buf).device
+
+    def _pointers(self):
+        if self._buf is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        p = self._buf.data_ptr()
+        return p, p + (-(-self.rows // 32) * 32) * (-(-self.cols // 16) * 16)
 
     @staticmethod
     def padded(rows: int, cols: int):
@@ -141,22 +166,26 @@ class Act8:
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Act8":
         r, p = cls.padded(rows, cols)
-        return cls(torch.empty((r, p), dtype=_I8, device=device),
-                   torch.empty((r // L.ACT8_ROWS, p), dtype=_U8, device=device), rows, cols)
+        buf = torch.empty(r * p + r // L.ACT8_ROWS * p, dtype=_U8, device=device)
+        _tensor(buf, "codes")
+        return _of_buffer(buf, rows, cols)
 
     @property
     def nbytes(self) -> int:
-        return self._codes.numel() + self._scales.numel()
+        r, p = self.padded(self.rows, self.cols)
+        return r * p + r // L.ACT8_ROWS * p
+
+
+def _of_buffer(buf: torch.Tensor, rows: int, cols: int) -> Act8:
+    a = Act8.__new__(Act8)
+    a._buf, a._codes, a._scales, a.rows, a.cols = buf, None, None, rows, cols
+    return a
 
 
 def _new_act8(like: torch.Tensor, rows: int, cols: int) -> Act8:
-    """Act8.empty on a tensor's device, without checking what was made here."""
-    r, p = -(-rows // 32) * 32, -(-cols // 16) * 16
-    a = Act8.__new__(Act8)
-    a._codes = like.new_empty((r, p), dtype=_I8)
-    a._scales = like.new_empty((r >> 5, p), dtype=_U8)
-    a.rows, a.cols = rows, cols
-    return a
+    """Act8.empty on a tensor's device."""
+    blocks = -(-rows // 32)
+    return _of_buffer(like.new_empty(blocks * 33 * (-(-cols // 16) * 16), dtype=_U8), rows, cols)
 
 
 def _act8(a, what: str, rows: int, cols: int, device):
@@ -165,10 +194,9 @@ def _act8(a, what: str, rows: int, cols: int, device):
         raise TypeError(f"{what} must be an Act8")
     if a.rows != rows or a.cols != cols:
         raise ValueError(f"{what} must hold {(rows, cols)}, got {(a.rows, a.cols)}")
-    codes = a._codes
-    if codes.device != device:
-        raise ValueError(f"{what} must be on {device}, got {codes.device}")
-    return codes.data_ptr(), a._scales.data_ptr()
+    if a.device != device:
+        raise ValueError(f"{what} must be on {device}, got {a.device}")
+    return a._pointers()
 
 
 @_on_stream
@@ -191,19 +219,21 @@ def act8_load(a: Act8, dtype=torch.bfloat16, out: torch.Tensor | None = None) ->
     """The values of a checkpoint, in `dtype` (or in `out`, of its own type)."""
     if not isinstance(a, Act8):
         raise TypeError("a must be an Act8")
-    codes, rows, cols = a._codes, a.rows, a.cols
-    dev = codes.device
+    held = a._codes if a._buf is None else a._buf
+    rows, cols = a.rows, a.cols
+    dev = held.device
     s = _stream(dev)
+    c, e = a._pointers()
     if out is None:
         if dtype not in _DTYPES:
             raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-        out = codes.new_empty((rows, cols), dtype=dtype)
+        out = held.new_empty((rows, cols), dtype=dtype)
         ld = cols
     else:
         ld = _matrix(out, "out", None, rows, cols, dev)
         dtype = out.dtype
-    L.check(L.lib().shampoo4_act8_load(_DTYPES[dtype], rows, cols, codes.data_ptr(), a._scales.data_ptr(),
-                                       out.data_ptr(), ld, s), "shampoo4_act8_load")
+    L.check(L.lib().shampoo4_act8_load(_DTYPES[dtype], rows, cols, c, e, out.data_ptr(), ld, s),
+            "shampoo4_act8_load")
     return out
 
 
@@ -234,13 +264,13 @@ def activation_forward(gate: torch.Tensor, up: torch.Tensor | None = None, kind:
     gc = ge = uc = ue = hc = he = 0
     if checkpoint:
         g8 = _new_act8(gate, rows, cols)
-        gc, ge = g8._codes.data_ptr(), g8._scales.data_ptr()
+        gc, ge = g8._pointers()
         if up is not None:
             u8 = _new_act8(gate, rows, cols)
-            uc, ue = u8._codes.data_ptr(), u8._scales.data_ptr()
+            uc, ue = u8._pointers()
     if save_output:
         h8 = _new_act8(gate, rows, cols)
-        hc, he = h8._codes.data_ptr(), h8._scales.data_ptr()
+        hc, he = h8._pointers()
     L.check(L.lib().shampoo4_activation_forward(_KINDS[kind], _DTYPES[dtype], rows, cols, gate.data_ptr(), ldg, up_ptr,
                                                 ldu, out.data_ptr(), ldh, gc, ge, uc, ue, hc, he, s),
             "shampoo4_activation_forward")
@@ -415,10 +445,12 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, out: torch.Tenso
     tp = _ids(targets, rows, "targets", dev)
     if out is None:
         out = logits.new_empty(rows, dtype=_F32)
-    op = _vector(out, rows, "out", _F32, dev)
+        op = out.data_ptr()
+    else:
+        op = _vector(out, rows, "out", _F32, dev)
     lib = L.lib()
     dt = _DTYPES[logits.dtype]
-    ws, wp, wb = _workspace(workspace, lib.shampoo4_policy_loss_workspace_bytes(dt, rows, vocab), logits)
+    ws, wp, wb = _workspace(workspace, lib.shampoo4_token_logprobs_workspace_bytes(dt, rows, vocab), logits)
     L.check(lib.shampoo4_token_logprobs(dt, _ID_BYTES[targets.dtype], rows, vocab, logits.data_ptr(), ldz, tp, op, wp,
                                         wb, s), "shampoo4_token_logprobs")
     return out

@@ -171,7 +171,9 @@ SHAMPOO4_API shampoo4_status shampoo4_policy_loss(const shampoo4_policy_config* 
                                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* logp[t] alone, for every row (the old and reference log-probabilities of a rollout); 0
- * for a target outside [0, vocab).  Workspace as for shampoo4_policy_loss. */
+ * for a target outside [0, vocab).  Its workspace (NULL when the size is 0) is not larger than
+ * shampoo4_policy_loss's. */
+SHAMPOO4_API size_t shampoo4_token_logprobs_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab);
 SHAMPOO4_API shampoo4_status shampoo4_token_logprobs(shampoo4_dtype dtype, int32_t id_bytes, int64_t rows,
                                                      int64_t vocab, const void* logits, int64_t ldlogits,
                                                      const void* targets, float* logp,
