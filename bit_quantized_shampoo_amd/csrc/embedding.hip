@@ -7,7 +7,8 @@
 //     9 bits.  A wave ranks 64 ids at a time: a ballot a bit gives each lane the lanes that
 //     share its digit, its rank among them and their number.  Up to SMALL_T tokens it is one
 //     launch, each workgroup sorting a range of ids in LDS; beyond, a pass is two launches
-//     over blocks of SORT_TILE tokens (digit counts, then ranks and scatter).
+//     over blocks of SORT_TILE tokens (digit counts, then ranks and scatter).  Up to RANK_T
+//     tokens there are no digits: a token's place is counted.
 //     Without accumulation the other workgroups of these launches write G's zeros: the fill
 //     is bound by HBM and the sort by latency, so the sort costs little beside it.
 //  2. Sums of runs of equal ids, cut at every CHUNK sorted positions: one wave per piece (short
@@ -39,6 +40,9 @@ constexpr int RADIX_BITS = 9;                // most bits of a digit
 constexpr int BINS = 1 << RADIX_BITS;
 constexpr int SMALL_T = 16384;               // tokens of the one-launch sort: 16 waves of up to 16 rounds
 constexpr int SMALL_WAVES = 16;
+constexpr int RANK_T = 4096;                 // tokens of the sort by counting
+constexpr int RANK_LANES = 32;               // lanes that count for an item
+constexpr int RANK_ITEMS = 1024 / RANK_LANES;
 constexpr int TILE_WAVES = 8;
 constexpr int TILE_ROUNDS = 8;
 constexpr int SORT_TILE = TILE_WAVES * TILE_ROUNDS * 64;
@@ -268,6 +272,57 @@ __global__ __launch_bounds__(1024) void sort_small_kernel(const void* ids, int i
     for (int i = tid; i < (int)n; i += 1024) {
         stg(skey + out + i, lo + (buf[i] >> pos_bits));
         stg(spos + out + i, buf[i] & ((1u << pos_bits) - 1));
+    }
+}
+
+// Up to RANK_T tokens: an item's place is the number of ids below its own and of equal ones
+// before it, counted among all of them in LDS.  A workgroup places RANK_ITEMS items,
+// RANK_LANES lanes an item; no passes, and no barrier but the one behind the loads.  Its
+// work grows with the tokens' square, so it ends where the digits win.  Measured, by digits
+// and by counting: 64 tokens 8.2 and 2.8 us, 1000 9.5 and 4.0, 4096 10.8 and 6.9; with zeros of 33
+// MB beside them 4096 14.2 and 11.8, with 268 MB 37.1 and 39.5.
+__global__ __launch_bounds__(1024) void sort_rank_kernel(const void* ids, int id64, int64_t vocab, int tokens, int sorters,
+                                                         uint32_t* skey, uint32_t* spos, Fill fill) {
+    typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+    __shared__ U4 keys[RANK_T / 4];
+    if ((int)blockIdx.x >= sorters) {
+        fill_zeros(fill, blockIdx.x - sorters, gridDim.x - sorters);
+        return;
+    }
+    const int tid = threadIdx.x;
+    uint32_t key[RANK_T / 1024];
+#pragma unroll
+    for (int r = 0; r < RANK_T / 1024; ++r) key[r] = key_at(ids, id64, vocab, min(tid + r * 1024, tokens - 1));
+#pragma unroll
+    for (int r = 0; r < RANK_T / 1024; ++r)
+        // above every id behind the last token
+        ((uint32_t*)keys)[tid + r * 1024] = tid + r * 1024 < tokens ? key[r] : 0xffffffffu;
+    __syncthreads();
+    // ids before the item count if they are below mine + 1, ids behind it below mine; of the
+    // four of the read that holds the item, those before it are looked at again
+    const int i = blockIdx.x * RANK_ITEMS + tid / RANK_LANES, lane = tid % RANK_LANES;
+    const uint32_t mine = ((const uint32_t*)keys)[min(i, RANK_T - 1)];
+    uint32_t place = 0;
+    static_assert(RANK_T % (16 * RANK_LANES) == 0, "whole turns");
+    for (int j0 = 0; j0 < tokens; j0 += 16 * RANK_LANES) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + (u * RANK_LANES + lane) * 4;
+            const U4 k = keys[j >> 2];
+            const uint32_t below = mine + (j + 3 < i ? 1u : 0u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) place += k[q] < below ? 1u : 0u;
+        }
+    }
+    const U4 k = keys[min(i, RANK_T - 1) >> 2];
+    if (lane == 0)
+#pragma unroll
+        for (int q = 0; q < 3; ++q) place += q < (i & 3) && k[q] == mine ? 1u : 0u;
+#pragma unroll
+    for (int o = RANK_LANES / 2; o >= 1; o >>= 1) place += (uint32_t)__shfl_xor((int)place, o);
+    if (lane == 0 && i < tokens) {
+        stg(skey + place, mine);
+        stg(spos + place, (uint32_t)i);
     }
 }
 
@@ -707,12 +762,17 @@ hipError_t launch_embedding_grad(shampoo4_dtype dtype, const EmbedGrad& e, void*
     };
     uint32_t *skey, *spos;
     if (e.tokens == 0 && fill_bytes == 0) return hipSuccess;
-    if (e.tokens == 0 || p.small) {
+    if (e.tokens <= RANK_T || p.small) {
         skey = (uint32_t*)(ws + p.off_key[0]);
         spos = (uint32_t*)(ws + p.off_pos[0]);
-        const int parts = e.tokens == 0 ? 0 : p.parts;       // no tokens: nothing is read
-        S4_LAUNCH(sort_small_kernel, dim3(parts + fill_blocks(parts, 1, 4)), dim3(1024), 0, stream, e.ids, e.id64, e.vocab,
-                  (int)e.tokens, parts, p.range, p.passes, p.digit, p.pos_bits, skey, spos, fill);
+    }
+    if (e.tokens <= RANK_T) {
+        const int sorters = (int)(e.tokens + RANK_ITEMS - 1) / RANK_ITEMS;    // no tokens: nothing is read
+        S4_LAUNCH(sort_rank_kernel, dim3(sorters + fill_blocks(sorters, 1, 4)), dim3(1024), 0, stream, e.ids, e.id64,
+                  e.vocab, (int)e.tokens, sorters, skey, spos, fill);
+    } else if (p.small) {
+        S4_LAUNCH(sort_small_kernel, dim3(p.parts + fill_blocks(p.parts, 1, 4)), dim3(1024), 0, stream, e.ids, e.id64,
+                  e.vocab, (int)e.tokens, p.parts, p.range, p.passes, p.digit, p.pos_bits, skey, spos, fill);
     } else {
         fill.parts = 2 * p.passes;
         const uint32_t nf = fill_blocks(p.nblk, fill.parts, 4);

@@ -103,6 +103,20 @@ def test_grad(t, v, d, dt, how, accumulate):
 
 
 @pytest.mark.parametrize("t,v,d,dt,how,idt", [
+    (2, 2, 3, "f32", "few", torch.int64), (31, 6, 8, "f32", "few", torch.int32), (33, 1 << 20, 2, "f32", "uniform", torch.int64),
+    (1024, 30, 16, "bf16", "zipf", torch.int32), (4095, 900, 8, "f32", "zipf", torch.int64),
+    (4096, 1, 8, "bf16", "one", torch.int32), (4096, 1 << 24, 1, "f32", "uniform", torch.int64),
+    (4097, 900, 8, "f32", "zipf", torch.int32), (5000, 3, 24, "f16", "few", torch.int64),
+    (8191, 5003, 16, "f32", "uniform", torch.int64), (16383, 70000, 8, "bf16", "zipf", torch.int32),
+])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_around_the_sorts_limits(t, v, d, dt, how, idt, accumulate):
+    """Few tokens are placed by counting, more by digits in ranges of ids."""
+    require_gpu()
+    _check_grad(t, v, d, dt, how, accumulate, idt)
+
+
+@pytest.mark.parametrize("t,v,d,dt,how,idt", [
     (16385, 511, 16, "f32", "zipf", torch.int32), (20000, 300000, 8, "bf16", "uniform", torch.int64),
     (40000, 65536, 8, "f32", "zipf", torch.int64), (30000, 2, 8, "f32", "few", torch.int32),
     (9000, 1 << 20, 8, "bf16", "uniform", torch.int32), (9000, 1 << 24, 1, "f32", "uniform", torch.int64),
