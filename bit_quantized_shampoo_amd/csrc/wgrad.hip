@@ -26,6 +26,11 @@
 // spreads of the staging over the units.  f32 dY 5461 x 4096 x 4096 430 us, f16 8192 x 4096 x
 // 4096 432, the same number of matrix-core products; 16384 x 1024 x 4096 bf16 136 us (library
 // 155), 8192 x 1024 x 1024 32 (52), 4096 x 4096 x 1024 48 (43).
+//
+// On the 128 x 128 tile a slice of 64 tokens takes 0.65 us a workgroup, alone or with every CU
+// busy, four times its products: the chain of LDS reads, products, staging and the barrier.
+// Two slices in registers take the same time; four waves of 64 x 64 instead of eight
+// of 64 x 32, with two thirds of the LDS reads, take 20% more.
 #include <algorithm>
 
 #include "train_common.hpp"
@@ -349,7 +354,7 @@ __global__ __launch_bounds__(256) void wgrad_sum_kernel(WGrad w, int splits) {
             s = ((s + a) + b) + c;
         }
         for (; k < splits; ++k) s += *(G*)(w.parts + k * n + i);
-        const int64_t r = i / w.cols;
+        const int64_t r = w.n == 1 ? 0 : i / w.cols;
         G* p = (G*)(w.g + r * w.ldg + (i - r * w.cols));
         s *= w.alpha;
         if (w.beta != 0.f) s += w.beta * *p;
@@ -439,13 +444,18 @@ hipError_t launch_wgrad(shampoo4_dtype dtype, const WGrad& w, hipStream_t stream
     }
     if (e != hipSuccess) return e;
     if (part) {
-        const bool four = w.cols % 4 == 0;
-        const int64_t threads = w.n * w.cols / (four ? 4 : 1);
+        WGrad v = w;
+        if (w.ldg == w.cols) {                               // contiguous rows are one
+            v.n = 1;
+            v.cols = v.ldg = w.n * w.cols;
+        }
+        const bool four = v.cols % 4 == 0;
+        const int64_t threads = v.n * v.cols / (four ? 4 : 1);
         const dim3 sg((uint32_t)std::min<int64_t>((threads + 255) / 256, 4096));
         if (four)
-            S4_LAUNCH(wgrad_sum_kernel<4>, sg, dim3(256), 0, stream, w, p.splits);
+            S4_LAUNCH(wgrad_sum_kernel<4>, sg, dim3(256), 0, stream, v, p.splits);
         else
-            S4_LAUNCH(wgrad_sum_kernel<1>, sg, dim3(256), 0, stream, w, p.splits);
+            S4_LAUNCH(wgrad_sum_kernel<1>, sg, dim3(256), 0, stream, v, p.splits);
     }
     return hipGetLastError();
 }

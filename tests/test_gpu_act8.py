@@ -261,6 +261,13 @@ def test_weight_grad_accumulates_into_a_view(dt):
     _wgrad_case(5000, 70, 131, dt, seed=4, alpha=-2.0, beta=0.25, pad=3)
 
 
+@pytest.mark.parametrize("n,c", [(70, 131), (64, 131), (1, 7), (5, 260)])
+def test_weight_grad_joins_row_ranges_of_contiguous_outputs(n, c):
+    require_gpu()
+    _wgrad_case(2000, n, c, "f32", seed=n + c, alpha=1.5, beta=-0.5)
+    _wgrad_case(4000, n, c, "bf16", seed=n + c + 1)
+
+
 def test_weight_grad_large_and_deterministic():
     """A layer of the transformer shapes: against float64 on the GPU, twice the same bits, and
     beta = 0 reads nothing of a NaN-filled output."""
