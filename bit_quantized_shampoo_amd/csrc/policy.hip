@@ -1,7 +1,7 @@
 // Clipped policy loss with a KL term on logits, forward and backward in one pass over them,
 // and the token log-probabilities alone.
 //
-// A row's softmax statistics are a maximum and a sum of exp(z - maximum), in fp32:
+// A row's softmax statistics are a maximum and a sum of exponentials beside it, in fp32:
 // logp = (z_y - m) - log s, and dZ = c ([v = y] - exp(z - m) / s) with one coefficient c a
 // row.  Two schedules:
 //  * Row kernel: a workgroup keeps a whole row in registers (64 registers of a thread), so
@@ -29,23 +29,39 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float NEG_INF = -__builtin_inff();
+constexpr float WHOLE_REF = 1073741824.f;    // 2^30
 
-// The sums' reference point is kept in powers of two and whole: R = round(m log2e) for a
-// maximum m, so that z - reference = z log2e - R is one fused multiply-add with one rounding,
-// two sums are brought together by an exact power of two, and
-// logp = ln2 ((z_y log2e - R) - log2 s) meets no rounding of the reference.  A set with no
-// probability (every logit -infinity) has R = -infinity and the sum 0.
-__device__ __forceinline__ float whole_ref(float m) { return m == NEG_INF ? NEG_INF : rintf(m * LOG2E); }
-__device__ __forceinline__ float base_of(float ref) { return ref == NEG_INF ? 0.f : ref; }
-__device__ __forceinline__ float exp_at(float z, float base) {
-    return __builtin_amdgcn_exp2f(fmaf(z, LOG2E, -base));
+// The sums' reference point goes by a maximum m.  Up to |m| = 2^30 it is kept in powers of two
+// and whole, c = round(m log2e): z - reference = z log2e - c is one fused multiply-add with
+// one rounding, two sums are brought together by an exact power of two, and
+// logp = ln2 ((z_y log2e - c) - log2 s) meets no rounding of the reference.  c is then off by
+// at most half its spacing, 64, so the maximum's own term is within 2^-64 .. 2^64.  For larger
+// m the spacing passes the exponent's range, and the reference is m itself, exactly, with
+// differences taken as they are: floats beyond 2^30 are 128 or more apart, so exp2(z - m) is
+// 1 or 0 (below 2^-127) as exp(z - m) is.  So are two sums of which one has a reference of
+// each kind: the smaller one is 0.  A set with no probability (every logit -infinity) has
+// m = -infinity and the sum 0.
+struct Base {
+    float k, c;               // exp(z - reference) = exp2(z k - c)
+};
+__device__ __forceinline__ Base base_of(float m) {
+    if (m == NEG_INF) return {LOG2E, 0.f};
+    return fabsf(m) <= WHOLE_REF ? Base{LOG2E, rintf(m * LOG2E)} : Base{1.f, m};
 }
-// s times 2^(ref - base)
-__device__ __forceinline__ float rebase(float s, float ref, float base) {
-    return s * __builtin_amdgcn_exp2f(ref - base);
+__device__ __forceinline__ float exp_at(float z, Base b) {
+    return __builtin_amdgcn_exp2f(fmaf(z, b.k, -b.c));
 }
-__device__ __forceinline__ float log_prob(float zy, float base, float s) {
-    return LN2 * (fmaf(zy, LOG2E, -base) - __builtin_amdgcn_logf(s));
+// A set's sum s, of maximum m, brought to the reference `to` of a maximum that is not smaller (a
+// NaN sum stays NaN).
+__device__ __forceinline__ float rebase(float s, float m, Base to) {
+    const Base b = base_of(m);
+    return s * (m != NEG_INF && b.k == to.k ? __builtin_amdgcn_exp2f(b.c - to.c) : 0.f);
+}
+__device__ __forceinline__ float log_prob(float zy, Base b, float s) {
+    const float l = __builtin_amdgcn_logf(s);
+    if (b.k != 1.f && fabsf(zy) <= WHOLE_REF) return LN2 * (fmaf(zy, b.k, -b.c) - l);
+    // beyond, z_y log2e may pass fp32's range where logp does not
+    return (zy - (b.k == 1.f ? b.c : LN2 * b.c)) - LN2 * l;
 }
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -72,7 +88,7 @@ __device__ __forceinline__ float max8(float m, floatx8 f) {
     for (int j = 0; j < 8; ++j) m = fmaxf(m, f[j]);
     return m;
 }
-__device__ __forceinline__ float add_exp8(float s, floatx8 f, float base) {
+__device__ __forceinline__ float add_exp8(float s, floatx8 f, Base base) {
     float a = 0.f, b = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -114,7 +130,7 @@ __device__ __forceinline__ RowTerm row_term(const Policy& p, int64_t t, float lo
 template <class T, int THREADS, int NV>
 __global__ __launch_bounds__(THREADS) void policy_row_kernel(Policy p, float* __restrict__ terms) {
     constexpr int WAVES = THREADS / 64;
-    __shared__ float wref[WAVES], wsum[WAVES], zy;
+    __shared__ float wmax[WAVES], wsum[WAVES], zy;
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int64_t t = blockIdx.x;
     const T* z = (const T*)p.logits + t * p.ldz;
@@ -150,8 +166,8 @@ __global__ __launch_bounds__(THREADS) void policy_row_kernel(Policy p, float* __
         m = max8(m, Vec8<T>::get(r[j]));
         unpack_again(r[j]);
     }
-    float ref = whole_ref(wave_max(m));
-    float base = base_of(ref);
+    m = wave_max(m);
+    Base base = base_of(m);
     float s = exp_at(last, base);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -160,15 +176,15 @@ __global__ __launch_bounds__(THREADS) void policy_row_kernel(Policy p, float* __
     }
     s = wave_add(s);
     if (lane == 0) {
-        wref[wv] = ref;
+        wmax[wv] = m;
         wsum[wv] = s;
     }
     __syncthreads();
     // every wave joins the waves' sums, lane i taking wave i's
-    ref = lane < WAVES ? wref[lane] : NEG_INF;
+    m = lane < WAVES ? wmax[lane] : NEG_INF;
     s = lane < WAVES ? wsum[lane] : 0.f;
-    base = base_of(wave_max(ref));
-    s = wave_add(rebase(s, ref, base));
+    base = base_of(wave_max(m));
+    s = wave_add(rebase(s, m, base));
     const float logp = log_prob(zy, base, s);
     if (tid == 0 && p.logp) stg(p.logp + t, logp);
     if (!p.train) return;
@@ -199,7 +215,7 @@ __global__ __launch_bounds__(THREADS) void policy_row_kernel(Policy p, float* __
 // -- split rows --------------------------------------------------------------------------
 
 struct Pieces {
-    float* stat;              // [rows][pieces][2]: reference and sum
+    float* stat;              // [rows][pieces][2]: maximum and sum
     float* zy;                // [rows] target logit
     int64_t pieces;           // per row
     int64_t vecs;             // vectors per piece
@@ -207,7 +223,7 @@ struct Pieces {
 
 template <class T>
 __global__ __launch_bounds__(256) void policy_part_kernel(Policy p, Pieces q) {
-    __shared__ float wref[4], wsum[4];
+    __shared__ float wmax[4], wsum[4];
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
     const int64_t t = blockIdx.x / q.pieces, piece = blockIdx.x - t * q.pieces;
     const int64_t y = target_of(p, t);
@@ -216,7 +232,7 @@ __global__ __launch_bounds__(256) void policy_part_kernel(Policy p, Pieces q) {
     const int64_t nfull = p.vocab >> 3;
     const int tail = (int)p.vocab & 7;
     const int64_t v0 = piece * q.vecs, v1 = min(nfull, v0 + q.vecs);
-    float ref = NEG_INF, s = 0.f;
+    float top = NEG_INF, s = 0.f;
     for (int64_t v = v0 + tid; v < v1; v += 1024) {
         typename Vec8<T>::Raw r[4];
 #pragma unroll
@@ -224,33 +240,34 @@ __global__ __launch_bounds__(256) void policy_part_kernel(Policy p, Pieces q) {
             r[j] = no_logits<T>();
             if (v + j * 256 < v1) r[j] = load8(z + (v + j * 256) * 8);
         }
-        float m = NEG_INF;
+        float m = top;
 #pragma unroll
         for (int j = 0; j < 4; ++j) m = max8(m, Vec8<T>::get(r[j]));
-        const float top = fmaxf(ref, whole_ref(m)), base = base_of(top);
-        s = rebase(s, ref, base);
-        ref = top;
+        const Base base = base_of(m);
+        s = rebase(s, top, base);
+        top = m;
 #pragma unroll
         for (int j = 0; j < 4; ++j) s = add_exp8(s, Vec8<T>::get(r[j]), base);
     }
     if (piece == q.pieces - 1 && tid < tail) {
         const float x = (float)z[nfull * 8 + tid];
-        const float top = fmaxf(ref, whole_ref(x)), base = base_of(top);
-        s = rebase(s, ref, base) + exp_at(x, base);
-        ref = top;
+        const float m = fmaxf(top, x);
+        const Base base = base_of(m);
+        s = rebase(s, top, base) + exp_at(x, base);
+        top = m;
     }
-    const float top = wave_max(ref);
-    s = wave_add(rebase(s, ref, base_of(top)));
+    const float m = wave_max(top);
+    s = wave_add(rebase(s, top, base_of(m)));
     if (lane == 0) {
-        wref[wv] = top;
+        wmax[wv] = m;
         wsum[wv] = s;
     }
     __syncthreads();
     if (tid == 0) {
-        float a = wref[0];
-        for (int w = 1; w < 4; ++w) a = fmaxf(a, wref[w]);
+        float a = wmax[0];
+        for (int w = 1; w < 4; ++w) a = fmaxf(a, wmax[w]);
         float b = 0.f;
-        for (int w = 0; w < 4; ++w) b += rebase(wsum[w], wref[w], base_of(a));
+        for (int w = 0; w < 4; ++w) b += rebase(wsum[w], wmax[w], base_of(a));
         float* o = q.stat + 2 * (t * q.pieces + piece);
         stg(o, a);
         stg(o + 1, b);
@@ -259,15 +276,16 @@ __global__ __launch_bounds__(256) void policy_part_kernel(Policy p, Pieces q) {
 }
 
 struct RowStat {
-    float base, s;
+    Base base;
+    float s;
 };
 // A row's statistics from its pieces, by one wave.
 __device__ __forceinline__ RowStat join_pieces(const Pieces& q, int64_t t) {
     const int lane = threadIdx.x & 63;
     const float* st = q.stat + 2 * t * q.pieces;
-    float ref = NEG_INF;
-    for (int64_t i = lane; i < q.pieces; i += 64) ref = fmaxf(ref, ldg(st + 2 * i));
-    const float base = base_of(wave_max(ref));
+    float m = NEG_INF;
+    for (int64_t i = lane; i < q.pieces; i += 64) m = fmaxf(m, ldg(st + 2 * i));
+    const Base base = base_of(wave_max(m));
     float s = 0.f;
     for (int64_t i = lane; i < q.pieces; i += 64) s += rebase(ldg(st + 2 * i + 1), ldg(st + 2 * i), base);
     return {base, wave_add(s)};
@@ -299,11 +317,11 @@ __device__ void few_rows_loss(const Policy& p, const Pieces& q) {
         float logp = 0.f;
         if (target_of(p, t) >= 0) {
             const float* st = q.stat + 2 * t * q.pieces;
-            float ref = NEG_INF;
-            for (int64_t i = lane; i < q.pieces; i += 16) ref = fmaxf(ref, ldg(st + 2 * i));
+            float m = NEG_INF;
+            for (int64_t i = lane; i < q.pieces; i += 16) m = fmaxf(m, ldg(st + 2 * i));
 #pragma unroll
-            for (int o = 8; o >= 1; o >>= 1) ref = fmaxf(ref, __shfl_xor(ref, o));
-            const float base = base_of(ref);
+            for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+            const Base base = base_of(m);
             float s = 0.f;
             for (int64_t i = lane; i < q.pieces; i += 16) s += rebase(ldg(st + 2 * i + 1), ldg(st + 2 * i), base);
 #pragma unroll
@@ -344,7 +362,8 @@ __global__ __launch_bounds__(256) void policy_grad_kernel(Policy p, Pieces q) {
     }
     const RowStat st = join_pieces(q, t);
     const float coef = row_term(p, t, log_prob(ldg(q.zy + t), st.base, st.s)).coef;
-    const float scale = -coef / st.s, base = st.base;
+    const float scale = -coef / st.s;
+    const Base base = st.base;
     for (int64_t v = v0 + tid; v < v1; v += 256) {
         floatx8 f = Vec8<T>::get(load8(z + v * 8));
 #pragma unroll

@@ -150,7 +150,8 @@ SHAMPOO4_API shampoo4_status shampoo4_embedding_grad(shampoo4_dtype dtype, int32
  * puts the mask and the normalisation into w (a mean over kept tokens: w = mask / sum of
  * mask).  A row with w = 0, or a target outside [0, vocab), is not read at all: its logp
  * and gradient are 0 and it adds nothing, whatever its logits, old, ref and advantage are.
- * A logit of -infinity has probability 0.
+ * Finite logits may be of any size (masks of -1e10 or of the type's lowest value too); one of
+ * -infinity has probability 0.
  * Outputs: loss, one fp32; logp, fp32 [rows], or NULL; dlogits [rows, vocab] of `dtype`, or
  * NULL for the loss alone (dlogits may be Z itself, with its leading dimension).  ref may
  * be NULL with kl_coef = 0 (it is then not read).

@@ -249,3 +249,49 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(dz[-70:], want[2]) and torch.equal(logp[-70:], want[1])
     assert abs(float(loss) - float(want[0])) <= 1e-5 * float(adv[-70:].abs().sum())
     assert bool((dz[-71] == 0).all()) and bool((dz[0] == 0).all()) and float(logp[:-70].abs().sum()) == 0
+
+
+def _masked_rows(rows, vocab, dt, low):
+    """Rows with finite masks of one size: words allowed in one place only, a masked tail, nothing but the mask, a
+    maximum of the mask's size above ordinary logits, and every 37th word allowed."""
+    c = _case(rows, vocab, dt)
+    z, y = c["z"], c["y"]
+    z[0, 20:] = low
+    y[0] = 7
+    z[1, vocab // 3:] = low
+    y[1] = vocab // 3 - 1
+    z[2] = low
+    z[3, vocab // 2] = -low
+    y[3] = vocab // 2
+    for t in range(4, rows):
+        z[t].masked_fill_(torch.arange(vocab, device="cuda") % 37 != 0, low)
+        y[t] = y[t] // 37 * 37
+    lp = o.log_softmax(_np(z))[np.arange(rows), y]
+    c["old"], c["ref"] = (lp - 0.1).astype(np.float32), (lp + 0.2).astype(np.float32)
+    return c
+
+
+MASKS = (-1e4, -1e9, -5e9, -1e10, -1e12, -1e15, -1e20, -1e30, -1e38, "lowest")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,vocab", [(4, 500), (70, 3001), (5, 30000), (66, 70001)])
+def test_finite_masks_of_any_size(rows, vocab, dt):
+    """A finite logit is a logit: masks of every size have the probability that the definition gives them (0 beside
+    ordinary logits, 1 / vocab in a row of nothing else).  The bounds are those of ordinary logits: differences to
+    the maximum carry |z - m| 2^-23, which the terms' own size exp(z - m) outweighs (x exp(-x) < 0.4)."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import token_logprobs
+    for low in MASKS:
+        low = torch.finfo(DT[dt]).min if low == "lowest" else low
+        c = _masked_rows(rows, vocab, dt, low)
+        announce(f"policy finite masks {rows}x{vocab} {dt} {low}")
+        got = _run(c, 0.05)
+        _check(c, 0.05, dt, got)
+        assert abs(float(got[1][2]) + np.log(vocab)) <= 2e-5 + 2.0 ** -21 * np.log(vocab)
+        # the rows' log-probabilities alone, also of a masked word and below a large maximum
+        y = c["y"].copy()
+        y[0], y[3] = vocab - 1, 1
+        lp = o.log_softmax(_np(c["z"]))[np.arange(rows), y]
+        got = _np(token_logprobs(c["z"], torch.from_numpy(y).cuda()))
+        assert np.all(np.abs(got - lp) <= 2e-5 + 2.0 ** -21 * np.abs(lp))
