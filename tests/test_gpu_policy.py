@@ -295,3 +295,42 @@ def test_finite_masks_of_any_size(rows, vocab, dt):
         lp = o.log_softmax(_np(c["z"]))[np.arange(rows), y]
         got = _np(token_logprobs(c["z"], torch.from_numpy(y).cuda()))
         assert np.all(np.abs(got - lp) <= 2e-5 + 2.0 ** -21 * np.abs(lp))
+
+
+KL_STEPS = (0.0, 1e-5, -1e-5, 1e-4, -1e-4, 1e-3, -1e-3, 1e-2, -1e-2, 0.1, -0.1, 0.3, -0.4, 0.49, -0.51, 0.7, 2.0, -3.0)
+
+
+@pytest.mark.parametrize("vocab", [5, 30000])
+def test_kl_term_near_the_reference(vocab):
+    """The KL term and its derivative are relative to themselves: exp(d) - d - 1 and 1 - exp(d) lose nothing where d
+    is near 0.  d is exact in fp32 for ref within a factor of 2 of logp; then a dozen roundings of a series, or an
+    expm1 within 2^-22 of at most 3.7 times the term: 2^-18 of the term covers both.  With A = 0 the gradient's
+    coefficient is the KL term's derivative alone; where rows are split it is taken at a log-probability joined in
+    another order, 2^-21 of it away from the one returned."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import policy_loss
+    rows, kl = len(KL_STEPS), 0.04
+    c = _case(rows, vocab, "f32")
+    y = torch.from_numpy(c["y"]).cuda()
+    zero, old = torch.zeros(rows, device="cuda"), torch.from_numpy(c["old"]).cuda()
+    one = torch.ones(rows, device="cuda")
+    announce(f"policy KL near the reference {vocab}")
+    logp = policy_loss(c["z"], y, old, zero, one, grad=False)[1]
+    ref = logp + torch.tensor(KL_STEPS, device="cuda")
+    _, again, dz = policy_loss(c["z"], y, old, zero, one, ref_logp=ref, kl_coef=kl)
+    assert torch.equal(again, logp)
+    d = _np(ref) - _np(logp)
+    coef = -kl * np.expm1(d)
+    moved = kl * np.exp(d) * 2.0 ** -21 * np.abs(_np(logp)) if vocab > 9000 else np.zeros(rows)
+    p = np.exp(o.log_softmax(_np(c["z"])))
+    hot = np.zeros_like(p)
+    hot[np.arange(rows), c["y"]] = 1
+    assert np.all(np.abs(_np(dz) - coef[:, None] * (hot - p)) <= (2.0 ** -18 * np.abs(coef) + moved)[:, None] * (p + hot) + 1e-37)
+    for t in range(rows):
+        # expm1(d) - d in float64, by its series where that is short
+        x = d[t]
+        k = x * x / 2 * (1 + x / 3 * (1 + x / 4 * (1 + x / 5))) if abs(x) < 1e-3 else np.expm1(x) - x
+        w = zero.clone()
+        w[t] = 1
+        loss = float(policy_loss(c["z"], y, old, zero, w, ref_logp=ref, kl_coef=kl, grad=False)[0])
+        assert abs(loss - kl * k) <= 2.0 ** -18 * kl * k and loss >= 0
