@@ -126,8 +126,10 @@ struct RowTerm {
 };
 __device__ __forceinline__ RowTerm row_term(const Policy& p, int64_t t, float logp) {
     const float w = ldg(p.weights + t), adv = ldg(p.adv + t);
-    const float r = expf(logp - ldg(p.old_logp + t));
-    const float plain = r * adv;
+    const float x = logp - ldg(p.old_logp + t);
+    const float r = expf(x);
+    // no advantage counts for nothing, also where a finite x has a ratio beyond fp32
+    const float plain = adv == 0.f && x < -NEG_INF ? 0.f : r * adv;
     const float clipped = fminf(fmaxf(r, 1.f - p.clip_low), 1.f + p.clip_high) * adv;
     // a NaN ratio or advantage stays NaN
     float l = plain <= clipped ? -plain : clipped <= plain ? -clipped : plain + clipped;

@@ -334,3 +334,17 @@ def test_kl_term_near_the_reference(vocab):
         w[t] = 1
         loss = float(policy_loss(c["z"], y, old, zero, w, ref_logp=ref, kl_coef=kl, grad=False)[0])
         assert abs(loss - kl * k) <= 2.0 ** -18 * kl * k and loss >= 0
+
+
+@pytest.mark.parametrize("vocab", [5, 30000])
+def test_ratio_that_overflows(vocab):
+    """exp(logp - old) beyond fp32: without an advantage it counts for nothing, with a positive one it is clipped."""
+    require_gpu()
+    c = _case(4, vocab, "f32")
+    c["old"] = (c["old"] - 200).astype(np.float32)
+    c["adv"] = np.array([0.0, 1.5, -0.0, 0.5], np.float32)
+    announce(f"policy ratio overflow {vocab}")
+    loss, _, dz = _run(c, 0.0)
+    want = -1.28 * float((c["w"].astype(np.float64) * c["adv"]).sum())
+    assert abs(float(loss) - want) <= 1e-6 * abs(want)
+    assert bool((dz == 0).all())
