@@ -206,25 +206,49 @@ __global__ __launch_bounds__(256) void act8_load_kernel(Act8Ptr in, T* __restric
 }
 
 // a(x) and a'(x) = sg + x sg (1 - sg) z'(x) with sg = 1 / (1 + exp(-z)): z = x (SiLU) or
-// 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU, tanh form).  No difference of near values, so
-// small and large arguments keep their relative precision.  The hardware's exp2 and
-// reciprocal are good to an ulp; what would cost more is the rounding of the argument
-// -z log2 e, |z| 2^-24 of the result, so its remainder is kept and applied, and the
-// reciprocal takes one Newton step.  Past 100 on either side the sigmoid is 0 or 1 in fp32; a
-// NaN comes back with the product by x.
+// 2 sqrt(2/pi) (x + 0.044715 x^3) (GELU, tanh form).  The hardware's exp2 and reciprocal are
+// good to an ulp; what would cost more is the rounding of the argument -z log2 e, |z| 2^-24
+// of the result, so its remainder is kept and applied, and the reciprocal takes one Newton
+// step.  Past 110 on either side the sigmoid is 0 or 1 in fp32; a NaN comes back with the
+// product by x.
 template <int KIND>
-__device__ __forceinline__ float act_sigmoid(float x) {
-    float z = KIND == SHAMPOO4_ACT_SILU ? x : 1.5957691216f * fmaf(0.044715f * x * x, x, x);
-    z = __builtin_amdgcn_fmed3f(z, -100.f, 100.f);
-    constexpr float HI = -1.44269502162933349609375f, LO = -1.925963033500e-8f;      // -log2 e
-    const float t = z * HI;
-    const float rest = fmaf(z, LO, fmaf(z, HI, -t));
-    float e = __builtin_amdgcn_exp2f(t);
-    e = fmaf(e * 0.693147180559945f, rest, e);
-    const float d = 1.f + e;
-    float y = __builtin_amdgcn_rcpf(d);
-    y = fmaf(fmaf(-d, y, 1.f), y, y);
-    return t > 126.f ? 0.f : y;
+__device__ __forceinline__ float act_argument(float x) {
+    const float z = KIND == SHAMPOO4_ACT_SILU ? x : 1.5957691216f * fmaf(0.044715f * x * x, x, x);
+    return __builtin_amdgcn_fmed3f(z, -110.f, 110.f);
+}
+constexpr float LOG2E = 1.44269502162933349609375f, LOG2E_LO = 1.925963033500e-8f;
+
+// Eight sigmoids.  Below z = -87.3 the exponential, or its reciprocal, leaves the normal range:
+// there sg = exp(z), taken 2^64 larger, is brought to the nearest subnormal number (0 from -103.3
+// on).  One look for eight values: a wave seldom has one so small.
+template <int KIND>
+__device__ __forceinline__ floatx8 act_sigmoids(const floatx8& x) {
+    floatx8 sg;
+    float low = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float z = act_argument<KIND>(x[j]);
+        low = fminf(low, z);
+        const float t = z * -LOG2E;
+        const float rest = fmaf(z, -LOG2E_LO, fmaf(z, -LOG2E, -t));
+        float e = __builtin_amdgcn_exp2f(t);
+        e = fmaf(e * 0.693147180559945f, rest, e);
+        const float d = 1.f + e;
+        const float y = __builtin_amdgcn_rcpf(d);
+        sg[j] = fmaf(fmaf(-d, y, 1.f), y, y);
+    }
+    if (__any(low < -87.f)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float z = act_argument<KIND>(x[j]);
+            const float t = z * LOG2E;
+            const float rest = fmaf(z, LOG2E_LO, fmaf(z, LOG2E, -t));
+            float e = __builtin_amdgcn_exp2f(t + 64.f);
+            e = fmaf(e * 0.693147180559945f, rest, e);
+            sg[j] = z < -87.f ? e * 0x1p-64f : sg[j];
+        }
+    }
+    return sg;
 }
 template <int KIND>
 __device__ __forceinline__ float act_derivative(float x, float sg) {
@@ -249,9 +273,7 @@ __global__ __launch_bounds__(256) void act_forward_kernel(ActForward a, int64_t 
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const floatx8 x = Vec8<T>::get(g[i]);
-        floatx8 h;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = x[j] * act_sigmoid<KIND>(x[j]);
+        floatx8 h = x * act_sigmoids<KIND>(x);
         if constexpr (GATED) h *= Vec8<T>::get(u[i]);
         g[i] = Vec8<T>::put(h);
         store_row<T, ROWS>(ph, a.ldh, i, g[i], t);
@@ -284,10 +306,10 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int64_
     for (int i = 0; i < ROWS; ++i) {
         const floatx8 x = act8_values(cg[i], sg);
         const floatx8 dx = Vec8<T>::get(d[i]);
-        floatx8 s, dg, du;
+        const floatx8 s = act_sigmoids<KIND>(x);
+        floatx8 dg, du;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            s[j] = act_sigmoid<KIND>(x[j]);
             dg[j] = dx[j] * act_derivative<KIND>(x[j], s[j]);
             du[j] = dx[j] * (x[j] * s[j]);
         }

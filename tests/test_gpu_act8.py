@@ -432,3 +432,32 @@ def test_captured_graphs():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activation_keeps_its_small_values(kind):
+    """Where the sigmoid is below fp32's normal range (z from -87.3 down to -103.3) it is held as a subnormal number,
+    half a step of 2^-149 from its value: the products with x and with a large factor are what the formula gives.
+    z itself is within 5 roundings of its value for GELU, so exp(z) is within 3 |z| 2^-23."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_load, activation_backward, activation_forward
+    x = np.linspace(-110.0, -84.0, 208) if kind == "silu" else np.linspace(-11.2, -9.6, 208)
+    g = torch.from_numpy(np.tile(x.astype(np.float32), (32, 1))).cuda()
+    for up in (1.0, 1e20):
+        announce(f"activation of small values {kind} up={up}")
+        u = torch.full_like(g, up)
+        h, g8, u8, _ = activation_forward(g, u, kind=kind)
+        xs = _np(g)
+        z, _ = o.act_argument(xs, kind)
+        ref = o.activation(xs, kind) * up
+        tol = np.abs(ref) * (3 * np.abs(z) + 16) * 2.0 ** -23 + 2.0 ** -149 * (np.abs(xs) + 1) * max(up, 1.0)
+        assert np.all(np.abs(_np(h) - ref) <= tol)
+        dh = torch.full_like(g, 1e15)
+        dg, du = activation_backward(dh, g8, u8, kind=kind)
+        xs, xu = _np(act8_load(g8, torch.float32)), _np(act8_load(u8, torch.float32))
+        z, dz = o.act_argument(xs, kind)
+        rel = (3 * np.abs(z) + 16) * 2.0 ** -23
+        ref = o.activation(xs, kind) * 1e15
+        assert np.all(np.abs(_np(du) - ref) <= np.abs(ref) * rel + 2.0 ** -149 * (np.abs(xs) + 1) * 1e15)
+        ref = o.activation_derivative(xs, kind) * xu * 1e15
+        assert np.all(np.abs(_np(dg) - ref) <= np.abs(ref) * 2 * rel + 2.0 ** -149 * (np.abs(xs * dz) + 2) * xu * 1e15)
