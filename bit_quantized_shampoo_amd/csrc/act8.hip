@@ -218,11 +218,12 @@ __device__ __forceinline__ float act_argument(float x) {
 }
 constexpr float LOG2E = 1.44269502162933349609375f, LOG2E_LO = 1.925963033500e-8f;
 
-// Eight sigmoids.  Below z = -87.3 the exponential, or its reciprocal, leaves the normal range:
+// Eight sigmoids, and 1 - sg as e sg, which keeps its digits where the difference would be of
+// near numbers.  Below z = -87.3 the exponential, or its reciprocal, leaves the normal range:
 // there sg = exp(z), taken 2^64 larger, is brought to the nearest subnormal number (0 from -103.3
 // on).  One look for eight values: a wave seldom has one so small.
 template <int KIND>
-__device__ __forceinline__ floatx8 act_sigmoids(const floatx8& x) {
+__device__ __forceinline__ floatx8 act_sigmoids(const floatx8& x, floatx8& other) {
     floatx8 sg;
     float low = 0.f;
 #pragma unroll
@@ -236,6 +237,7 @@ __device__ __forceinline__ floatx8 act_sigmoids(const floatx8& x) {
         const float d = 1.f + e;
         const float y = __builtin_amdgcn_rcpf(d);
         sg[j] = fmaf(fmaf(-d, y, 1.f), y, y);
+        other[j] = e * sg[j];
     }
     if (__any(low < -87.f)) {
 #pragma unroll
@@ -246,15 +248,17 @@ __device__ __forceinline__ floatx8 act_sigmoids(const floatx8& x) {
             float e = __builtin_amdgcn_exp2f(t + 64.f);
             e = fmaf(e * 0.693147180559945f, rest, e);
             sg[j] = z < -87.f ? e * 0x1p-64f : sg[j];
+            other[j] = z < -87.f ? 1.f : other[j];
         }
     }
     return sg;
 }
+// The two terms are of opposite signs for x < 0 and cancel at the derivative's root alone.
 template <int KIND>
-__device__ __forceinline__ float act_derivative(float x, float sg) {
+__device__ __forceinline__ float act_derivative(float x, float sg, float other) {
     // bounded where the sigmoid is 0 or 1 and the product below is 0, so that it stays 0
     const float dz = KIND == SHAMPOO4_ACT_SILU ? 1.f : 1.5957691216f * fmaf(0.134145f, fminf(x * x, 1e8f), 1.f);
-    return fmaf(x * sg * (1.f - sg), dz, sg);
+    return fmaf(x * sg * other, dz, sg);
 }
 
 template <class T, int ROWS, int KIND, bool GATED>
@@ -273,7 +277,8 @@ __global__ __launch_bounds__(256) void act_forward_kernel(ActForward a, int64_t 
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const floatx8 x = Vec8<T>::get(g[i]);
-        floatx8 h = x * act_sigmoids<KIND>(x);
+        floatx8 other;
+        floatx8 h = x * act_sigmoids<KIND>(x, other);
         if constexpr (GATED) h *= Vec8<T>::get(u[i]);
         g[i] = Vec8<T>::put(h);
         store_row<T, ROWS>(ph, a.ldh, i, g[i], t);
@@ -306,11 +311,11 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackward a, int64_
     for (int i = 0; i < ROWS; ++i) {
         const floatx8 x = act8_values(cg[i], sg);
         const floatx8 dx = Vec8<T>::get(d[i]);
-        const floatx8 s = act_sigmoids<KIND>(x);
-        floatx8 dg, du;
+        floatx8 other, dg, du;
+        const floatx8 s = act_sigmoids<KIND>(x, other);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            dg[j] = dx[j] * act_derivative<KIND>(x[j], s[j]);
+            dg[j] = dx[j] * act_derivative<KIND>(x[j], s[j], other[j]);
             du[j] = dx[j] * (x[j] * s[j]);
         }
         if constexpr (GATED) dg *= act8_values(cu[i], su);

@@ -461,3 +461,27 @@ def test_activation_keeps_its_small_values(kind):
         assert np.all(np.abs(_np(du) - ref) <= np.abs(ref) * rel + 2.0 ** -149 * (np.abs(xs) + 1) * 1e15)
         ref = o.activation_derivative(xs, kind) * xu * 1e15
         assert np.all(np.abs(_np(dg) - ref) <= np.abs(ref) * 2 * rel + 2.0 ** -149 * (np.abs(xs * dz) + 2) * xu * 1e15)
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_activation_gradient_keeps_its_last_bits(kind):
+    """For z in 10 .. 25 the derivative is 1 and a small term x (1 - sg) z' of it: the sigmoid's sum, its reciprocal
+    and the two last roundings are within 2^-24 each, and the term, 0.3% at most, adds (3 |z| 2^-23) of itself: 6 2^-24
+    of dh in all.  1 - sg taken as a difference would lose 2^-24 times x z' (15 to 60) more."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_load, act8_store, activation_backward
+    lo, hi = (10.0, 25.0) if kind == "silu" else (4.2, 6.3)
+    rng = np.random.default_rng(2)
+    # columns of several scales: each block's largest value is in one of them
+    x = rng.uniform(lo, hi, (64, 300)).astype(np.float32)
+    g8 = act8_store(torch.from_numpy(x).cuda())
+    xs = _np(act8_load(g8, torch.float32))
+    dh = torch.from_numpy(rng.standard_normal((64, 300)).astype(np.float32)).cuda()
+    announce(f"activation gradient's last bits {kind}")
+    dg, _ = activation_backward(dh, g8, kind=kind)
+    d = _np(dh)
+    ref = d * o.activation_derivative(xs, kind)
+    z, _ = o.act_argument(xs, kind)
+    on = (z >= 10) & (z <= 25)
+    assert on.mean() > 0.8
+    assert np.all((np.abs(_np(dg) - ref) <= 6 * 2.0 ** -24 * np.abs(d))[on])
