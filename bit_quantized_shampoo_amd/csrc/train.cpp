@@ -57,8 +57,8 @@ shampoo4_status workspace_ok(const void* ws, size_t bytes, size_t need) {
     } while (0)
 
 bool wgrad_shape_ok(int64_t rows, int64_t n, int64_t cols) {
-    // output tiles of at least 64 x 64, at most 512 threads each in a launch
-    return shape_ok(rows, cols) && n >= 1 && n <= kMaxDim && ((n + 63) / 64) * ((cols + 63) / 64) < (int64_t(1) << 23);
+    // output tiles of at least 128 x 128, 512 threads each: below 2^32 in a launch
+    return shape_ok(rows, cols) && n >= 1 && n <= kMaxDim && ((n + 127) / 128) * ((cols + 127) / 128) < (int64_t(1) << 23);
 }
 
 bool embed_shape_ok(int64_t tokens, int64_t vocab, int64_t dim) {

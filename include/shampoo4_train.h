@@ -110,7 +110,7 @@ SHAMPOO4_API shampoo4_status shampoo4_activation_backward(int32_t kind, shampoo4
  * they stand, an f16 or f32 dY is split exactly into two or three bf16 pieces.
  * rows = 0: G = beta * G.  The workspace (NULL when the size is 0) holds partial sums of
  * row ranges when the output alone cannot fill the GPU.
- * ESHAPE also from 2^23 output tiles of 64 x 64 on. */
+ * ESHAPE also from 2^23 output tiles of 128 x 128 on (512 GiB of G). */
 SHAMPOO4_API size_t shampoo4_act8_weight_grad_workspace_bytes(int64_t rows, int64_t n, int64_t cols);
 SHAMPOO4_API shampoo4_status shampoo4_act8_weight_grad(shampoo4_dtype dtype, int64_t rows, int64_t n, int64_t cols,
                                                        float alpha, const void* dy, int64_t lddy,

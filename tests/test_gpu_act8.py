@@ -485,3 +485,16 @@ def test_activation_gradient_keeps_its_last_bits(kind):
     on = (z >= 10) & (z <= 25)
     assert on.mean() > 0.8
     assert np.all((np.abs(_np(dg) - ref) <= 6 * 2.0 ** -24 * np.abs(d))[on])
+
+
+def test_weight_grad_of_half_a_billion_columns():
+    """An output of 2^22 tiles, as wide as one launch takes with two rows: every product is exact."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import act8_load, act8_store, act8_weight_grad
+    c = (1 << 29) + 16
+    announce("weight gradient 1 x 2 x (2^29 + 16)")
+    x8 = act8_store((torch.arange(c, dtype=torch.int32, device="cuda") % 61 - 30).to(torch.bfloat16).view(1, c))
+    g = act8_weight_grad(torch.tensor([[2.0, -1.0]], device="cuda").bfloat16(), x8)
+    x = act8_load(x8, torch.float32)[0]
+    assert torch.equal(g[1], -x) and torch.equal(g[0], x + x)
+    assert float(x[c - 1]) == (c - 1) % 61 - 30

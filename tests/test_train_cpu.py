@@ -210,3 +210,12 @@ def test_oracle_policy_gradient_is_the_difference():
             diff = (o.policy(zp, *args)[0] - o.policy(zm, *args)[0]) / (2 * h)
             assert abs(diff - dz[t, v]) < 1e-8
     assert np.all(dz[2] == 0)
+
+
+def test_weight_grad_takes_every_output_that_a_launch_covers():
+    """Up to 2^23 output tiles of 128 x 128 pass the check of shapes (and are refused here for their null operand)."""
+    f = _lib().shampoo4_act8_weight_grad
+    big = 1 << 18                                    # 2^22 tiles of 128 x 128, 2^24 of 64 x 64
+    assert f(L.BF16, 4, big, big, 1.0, None, big, P, P, 0.0, P, big, None, 0, None) == L.EINVAL
+    over = big // 2 * 3                              # above 2^23
+    assert f(L.BF16, 4, over, over, 1.0, None, over, P, P, 0.0, P, over, None, 0, None) == L.ESHAPE
