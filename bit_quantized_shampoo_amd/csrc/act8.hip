@@ -9,10 +9,12 @@
 //
 // Large shapes are bound by HBM: [16384, 4096] bf16 stored in 39.4 us (5.2 TB/s) and loaded
 // in 31.6 (6.4 TB/s; part of the codes is still in the last-level cache); gated SiLU of
-// [8192, 4096] bf16 with both checkpoints in 61.1 us forward (4.4 TB/s) and 48.2 backward
-// (5.6 TB/s).  The counters show each
+// [8192, 4096] bf16 with both checkpoints in 58.6 us forward (4.6 TB/s) and 47.6 backward
+// (5.7 TB/s).  The counters show each
 // input read once and each output written once.  Small shapes take one launch and one trip
-// to memory: [16, 1024] bf16 3.1 us stored, 2.6 loaded.
+// to memory: [16, 1024] bf16 3.0 us stored, 2.5 loaded.  Between them, GELU of [1000, 2309] fp32
+// takes 9.0 us forward and 6.6 backward, launches behind each other, where the bytes are 4.6 and
+// 4.1; rows that are not aligned are the least of it ([1000, 2304]: 8.8 and 6.2).
 //
 // ROWS is 8, or 2 while the wide tiles are fewer than one a SIMD, where what counts is how
 // long a lane takes and not the 128-byte runs of a row.  Measured with 8 and with 2 rows a

@@ -6,7 +6,8 @@
 // token, in bf16, and gfx950's transposing LDS read (four tokens of sixteen columns a group of
 // sixteen lanes) gives each lane the consecutive tokens that a matrix-core operand takes. X^ =
 // code * 2^k is a bf16 number exactly, and a bf16 dY is an operand as it stands; an f16 or f32
-// dY is split exactly into two or three bf16 pieces, one product each.
+// dY is split exactly into two or three bf16 pieces, one product each (what a value has below
+// 2^-133, the smallest bf16 number, is dropped: digits of fp32 values under 2^-110).
 //
 // Bound by the matrix cores.  A workgroup of eight waves holds 256 x 256 outputs in its
 // accumulators (128 a lane): the largest tile that two waves a SIMD leave registers for, so an
@@ -24,13 +25,16 @@
 // beside the products.  Measured and not better (all within 1%): more registers of loads in
 // flight, two units of operands ahead, wave priorities, one scale decoded for two rows, other
 // spreads of the staging over the units.  f32 dY 5461 x 4096 x 4096 430 us, f16 8192 x 4096 x
-// 4096 432, the same number of matrix-core products; 16384 x 1024 x 4096 bf16 136 us (library
-// 155), 8192 x 1024 x 1024 32 (52), 4096 x 4096 x 1024 48 (43).
+// 4096 432, the same number of matrix-core products; 16384 x 1024 x 4096 bf16 137 us (library
+// 156), 8192 x 1024 x 1024 33 (53), 4096 x 4096 x 1024 50 (44), 2048 x 2048 x 2048 28.5 (25.6).
 //
-// On the 128 x 128 tile a slice of 64 tokens takes 0.65 us a workgroup, alone or with every CU
-// busy, four times its products: the chain of LDS reads, products, staging and the barrier.
-// Two slices in registers take the same time; four waves of 64 x 64 instead of eight
-// of 64 x 32, with two thirds of the LDS reads, take 20% more.
+// The 128 x 128 tile is bound by what a CU issues, not by a chain of latencies: a slice of 64
+// tokens takes 0.60 us for one workgroup on the GPU, 0.71 with one on every CU, and 1.28 for two
+// that share a CU (16384 x 4096 x 2048 bf16 in 512 workgroups 329 us, half of it in 256 182;
+// kept to one a CU, 355).  Of a CU's busy clocks there LDS is active for 52% (98 KB of operand
+// reads and 32 KB of stores a slice), the matrix cores for 42%, and vector instructions issue
+// for 49%: the three hide each other little.  Two slices in registers take the same time; four
+// waves of 64 x 64 instead of eight of 64 x 32, with two thirds of the LDS reads, take 20% more.
 #include <algorithm>
 
 #include "train_common.hpp"

@@ -10,6 +10,10 @@ device.  Work is enqueued on `stream` (default: the current stream), and tensors
 allocates (outputs not passed in, workspaces) belong to that stream, so the caching
 allocator reuses them in its order.  Inputs used on another stream than their own are the
 caller's to order, and to keep, as with any PyTorch operator.
+
+None of these calls is recorded by autograd: an input that requires a gradient is read like
+any other, and the result is detached from it.  Each backward pass is a call of its own
+(activation_backward, act8_weight_grad, embedding_grad, the dlogits of policy_loss).
 """
 
 from __future__ import annotations

@@ -107,7 +107,8 @@ SHAMPOO4_API shampoo4_status shampoo4_activation_backward(int32_t kind, shampoo4
  *     G = alpha * dY^T X^ + beta * G      dY:[rows, n], X^:[rows, cols], G:[n, cols] fp32
  * the block gradient that shampoo4_step takes.  With beta = 0, G is not read.  Products
  * are exact and sums in fp32 on the bf16 matrix cores: X^ and a bf16 dY are operands as
- * they stand, an f16 or f32 dY is split exactly into two or three bf16 pieces.
+ * they stand, an f16 or f32 dY is split exactly into two or three bf16 pieces (what an fp32
+ * value has below 2^-133 is dropped).
  * rows = 0: G = beta * G.  The workspace (NULL when the size is 0) holds partial sums of
  * row ranges when the output alone cannot fill the GPU.
  * ESHAPE also from 2^23 output tiles of 128 x 128 on (512 GiB of G). */
