@@ -8,5 +8,6 @@ binding.  Build with ``python -m bit_quantized_shampoo_amd.build``.
 from ._lib import LIB_PATH, Shampoo4Error  # noqa: F401
 from .shampoo4 import (Shampoo4Blocks, Shampoo4Config, codebook, dequantize,  # noqa: F401
                        gemm_batched, inverse_root, plan, quantize)
-from .train import (Act8, act8_load, act8_store, act8_weight_grad, activation_backward,  # noqa: F401
-                    activation_forward, embedding, embedding_grad, policy_loss, token_logprobs)
+from .train import (Act8, Fp8, act8_load, act8_store, act8_weight_grad, activation_backward,  # noqa: F401
+                    activation_forward, block_norm_backward, block_norm_forward, dropout, embedding, embedding_grad,
+                    fp8_linear, fp8_load, fp8_store, fp8_store_weight, policy_loss, token_logprobs)

@@ -47,11 +47,15 @@ EXPORTED_TRAIN = [
     "shampoo4_activation_backward", "shampoo4_act8_weight_grad_workspace_bytes", "shampoo4_act8_weight_grad",
     "shampoo4_embedding", "shampoo4_embedding_grad_workspace_bytes", "shampoo4_embedding_grad",
     "shampoo4_policy_loss_workspace_bytes", "shampoo4_policy_loss", "shampoo4_token_logprobs_workspace_bytes",
-    "shampoo4_token_logprobs",
+    "shampoo4_token_logprobs", "shampoo4_fp8_bytes", "shampoo4_fp8_store", "shampoo4_fp8_store_weight",
+    "shampoo4_fp8_load", "shampoo4_fp8_linear_workspace_bytes", "shampoo4_fp8_linear", "shampoo4_dropout",
+    "shampoo4_block_norm_forward", "shampoo4_block_norm_workspace_bytes", "shampoo4_block_norm_backward",
 ]
 F32, BF16, F16 = 0, 1, 2
 ACT_SILU, ACT_GELU = 0, 1
 ACT8_ROWS, ACT8_PITCH = 32, 16
+FP8_BLOCK = 128
+BLOCK_NORM_COLS = 16384
 
 GRAFT_SGD, GRAFT_ADAM = 0, 1
 GEMM_AUTO, GEMM_FP32, GEMM_X3 = 0, 1, 2
@@ -87,6 +91,15 @@ class GraftIo(ctypes.Structure):
 class PolicyConfig(ctypes.Structure):
     _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
                 ("grad_scale", ctypes.c_float)]
+
+
+class DropoutConfig(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("reserved", ctypes.c_int32), ("seed", ctypes.c_uint64),
+                ("offset", ctypes.c_uint64), ("counter", ctypes.c_void_p)]
+
+
+class BlockNormConfig(ctypes.Structure):
+    _fields_ = [("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("dropout", DropoutConfig)]
 
 
 class Shampoo4Error(RuntimeError):
@@ -171,6 +184,19 @@ def lib() -> ctypes.CDLL:
                                       vp, vp, vp, i64, vp, sz, vp]),
         "shampoo4_token_logprobs_workspace_bytes": (sz, [i32, i64, i64]),
         "shampoo4_token_logprobs": (st, [i32, i32, i64, i64, vp, i64, vp, vp, vp, sz, vp]),
+        "shampoo4_fp8_bytes": (st, [i64, i64, i32, ctypes.POINTER(sz), ctypes.POINTER(sz)]),
+        "shampoo4_fp8_store": (st, [i32, i64, i64, vp, i64, vp, vp, vp]),
+        "shampoo4_fp8_store_weight": (st, [i32, i64, i64, vp, i64, vp, vp, vp, vp, vp]),
+        "shampoo4_fp8_load": (st, [i32, i64, i64, i32, vp, vp, vp, i64, vp]),
+        "shampoo4_fp8_linear_workspace_bytes": (sz, [i32, i64, i64, i64, i32]),
+        "shampoo4_fp8_linear": (st, [i32, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp, i32, vp, i64, vp, sz, vp]),
+        "shampoo4_dropout": (st, [ctypes.POINTER(DropoutConfig), i32, i64, i64, vp, i64, vp, i64, vp]),
+        "shampoo4_block_norm_forward": (st, [ctypes.POINTER(BlockNormConfig), i32, i64, i64, vp, i64, vp, i64, vp, vp,
+                                             i32, i64, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp]),
+        "shampoo4_block_norm_workspace_bytes": (sz, [i64, i64]),
+        "shampoo4_block_norm_backward": (st, [ctypes.POINTER(BlockNormConfig), i32, i64, i64, vp, i64, vp, i64, vp, i64,
+                                              vp, vp, vp, i64, vp, vp, vp, i32, i64, vp, i64, vp, i64, vp, vp, vp, i64,
+                                              vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

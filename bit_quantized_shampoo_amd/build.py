@@ -19,8 +19,8 @@ LIB = os.path.join(PKG, "libshampoo4.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gemm.hip", "gemm_x3.hip", "codec.hip", "qr.hip", "elementwise.hip", "graft.hip", "newton.hip", "diag.hip",
-           "scratch.hip", "gemm64.hip", "qr64.hip", "act8.hip", "wgrad.hip", "embedding.hip", "policy.hip", "train.cpp",
-           "runtime.cpp"]
+           "scratch.hip", "gemm64.hip", "qr64.hip", "act8.hip", "wgrad.hip", "embedding.hip", "policy.hip", "fp8.hip",
+           "linear.hip", "norm.hip", "dropout.hip", "train.cpp", "runtime.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

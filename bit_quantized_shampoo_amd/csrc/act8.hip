@@ -177,19 +177,6 @@ __global__ __launch_bounds__(256) void act8_store_kernel(const T* __restrict__ x
     encode_tile<T, ROWS>(r, out, act8_pitch(cols), t);
 }
 
-template <class T>
-__device__ __forceinline__ floatx8 saturate(floatx8 f) {
-    if constexpr (sizeof(T) == 2 && !__is_same(T, __bf16)) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            // a finite value beyond float16's range; NaN passes (both comparisons are false)
-            f[j] = f[j] > 65504.f ? 65504.f : f[j];
-            f[j] = f[j] < -65504.f ? -65504.f : f[j];
-        }
-    }
-    return f;
-}
-
 template <class T, int ROWS>
 __global__ __launch_bounds__(256) void act8_load_kernel(Act8Ptr in, T* __restrict__ x, int64_t ldx, int64_t rows,
                                                         int64_t cols, int64_t ntiles) {

@@ -1,0 +1,56 @@
+// Dropout's decisions (shampoo4_train.h): sixteen bits an element from the ten-round Philox
+// 4 x 32 generator of Salmon, Moraes, Dror and Shaw (2011).  One call of it, 20 wide
+// multiplications, serves eight columns.
+#pragma once
+
+#include "train_common.hpp"
+
+namespace s4 {
+
+struct Drop {
+    uint32_t threshold;       // dropped below; 0: nothing is
+    float scale;              // of what is kept
+    uint64_t seed, offset;
+    const uint64_t* counter;  // or NULL
+};
+
+// offset + counter, read once a thread
+__device__ __forceinline__ uint64_t drop_call(const Drop& d) {
+    return d.offset + (d.threshold && d.counter ? ldg(d.counter) : 0);
+}
+
+__device__ __forceinline__ u32x4 philox(uint32_t x0, uint32_t x1, uint64_t call, uint64_t seed) {
+    uint32_t x2 = (uint32_t)call, x3 = (uint32_t)(call >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)x0 * 0xd2511f53u, b = (uint64_t)x2 * 0xcd9e8d57u;
+        x0 = (uint32_t)(b >> 32) ^ x1 ^ k0;
+        x1 = (uint32_t)b;
+        x2 = (uint32_t)(a >> 32) ^ x3 ^ k1;
+        x3 = (uint32_t)a;
+        k0 += 0x9e3779b9u;
+        k1 += 0xbb67ae85u;
+    }
+    return u32x4{x0, x1, x2, x3};
+}
+
+// Bit j: column 8 col8 + j of the row is kept.
+__device__ __forceinline__ uint32_t drop_keep8(const Drop& d, uint64_t call, int64_t row, int64_t col8) {
+    const u32x4 w = philox((uint32_t)col8, (uint32_t)row, call, d.seed);
+    uint32_t keep = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t r = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
+        keep |= (r >= d.threshold ? 1u : 0u) << j;
+    }
+    return keep;
+}
+// Kept values scaled, others 0 whatever they were.
+__device__ __forceinline__ floatx8 drop8(floatx8 x, uint32_t keep, float scale) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = keep >> j & 1 ? x[j] * scale : 0.f;
+    return x;
+}
+
+}  // namespace s4

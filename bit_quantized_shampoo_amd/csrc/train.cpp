@@ -4,6 +4,7 @@
 
 #include <rocprofiler-sdk-roctx/roctx.h>
 
+#include "random.hpp"
 #include "train.hpp"
 
 using namespace s4;
@@ -84,6 +85,50 @@ shampoo4_status policy_call(const Policy& p, shampoo4_dtype dtype, int32_t id_by
     }
     S4_TRY(workspace_ok(workspace, workspace_bytes, policy_workspace_bytes(dtype, p.rows, p.vocab, p.train != 0)));
     return launched(launch_policy(dtype, p, workspace, as_stream(stream)));
+}
+
+// Codes and scales of a matrix: both, 16-byte and 4-byte aligned; none where nothing is there.
+shampoo4_status fp8_ok(const uint8_t* codes, const uint8_t* scales, int64_t rows) {
+    if (rows == 0) return SHAMPOO4_OK;
+    if (!codes || !scales) return SHAMPOO4_EINVAL;
+    return aligned(codes, 16) && aligned(scales, 4) ? SHAMPOO4_OK : SHAMPOO4_EALIGN;
+}
+
+// Tiles of 4 rows x 512 columns, 64 threads each, in a launch.
+bool stream_shape_ok(int64_t rows, int64_t cols) {
+    return shape_ok(rows, cols) && (rows + 3) / 4 * ((cols + 511) / 512) < (int64_t(1) << 24);
+}
+
+bool linear_shape_ok(int64_t rows, int64_t n, int64_t k) {
+    return shape_ok(rows, n) && k >= 1 && k <= kMaxDim &&
+           ((rows + 63) / 64) * ((n + 63) / 64) < (int64_t(1) << 22) && stream_shape_ok(rows, k);
+}
+
+bool block_shape_ok(int64_t rows, int64_t cols) {
+    return rows >= 0 && rows < (int64_t(1) << 24) && cols >= 1 && cols <= SHAMPOO4_BLOCK_NORM_COLS;
+}
+
+shampoo4_status drop_of(const shampoo4_dropout_config& c, Drop& d) {
+    if (!(c.p >= 0.f && c.p <= 1.f) || c.reserved != 0) return SHAMPOO4_EINVAL;
+    const double t = std::nearbyint((double)c.p * 65536.0);
+    if (t >= 65536.0) return SHAMPOO4_EINVAL;
+    if (!aligned(c.counter, 8)) return SHAMPOO4_EALIGN;
+    d = {(uint32_t)t, (float)(65536.0 / (65536.0 - t)), c.seed, c.offset, c.counter};
+    return SHAMPOO4_OK;
+}
+
+shampoo4_status block_config_ok(const shampoo4_block_norm_config* cfg) {
+    if (!cfg || !(cfg->eps >= 1e-30f) || !std::isfinite(cfg->eps) || !std::isfinite(cfg->residual_scale))
+        return SHAMPOO4_EINVAL;
+    return SHAMPOO4_OK;
+}
+
+// A gate: a vector of fp32, or a matrix of the call's type.
+shampoo4_status gate_ok(const void* gate, int32_t gate_rows, shampoo4_dtype dtype, int64_t rows, int64_t cols,
+                        int64_t ldgate) {
+    if (gate_rows != 0 && gate_rows != 1) return SHAMPOO4_EINVAL;
+    if (gate_rows) return matrix_ok(gate, dtype, rows, cols, ldgate);
+    return aligned(gate, 4) ? SHAMPOO4_OK : SHAMPOO4_EALIGN;
 }
 
 }  // namespace
@@ -256,6 +301,166 @@ shampoo4_status shampoo4_token_logprobs(shampoo4_dtype dtype, int32_t id_bytes, 
     p.ldz = ldlogits;
     p.id64 = id_bytes == 8;
     return policy_call(p, dtype, id_bytes, workspace, workspace_bytes, stream);
+}
+
+shampoo4_status shampoo4_fp8_bytes(int64_t rows, int64_t cols, int32_t block_rows, size_t* codes_bytes,
+                                   size_t* scales_bytes) {
+    if (!codes_bytes || !scales_bytes || (block_rows != 1 && block_rows != SHAMPOO4_FP8_BLOCK)) return SHAMPOO4_EINVAL;
+    if (!shape_ok(rows, cols)) return SHAMPOO4_ESHAPE;
+    *codes_bytes = (size_t)rows * ((cols + 127) / 128 * 128);
+    *scales_bytes = (size_t)((rows + block_rows - 1) / block_rows) * ((cols + 511) / 512 * 4);
+    return SHAMPOO4_OK;
+}
+
+shampoo4_status shampoo4_fp8_store(shampoo4_dtype dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                                   uint8_t* codes, uint8_t* scales, void* stream) {
+    CallRange range_("shampoo4_fp8_store");
+    if (!dtype_ok(dtype)) return SHAMPOO4_EINVAL;
+    if (!stream_shape_ok(rows, cols)) return SHAMPOO4_ESHAPE;
+    S4_TRY(matrix_ok(x, dtype, rows, cols, ldx));
+    S4_TRY(fp8_ok(codes, scales, rows));
+    return launched(launch_fp8_store(dtype, rows, cols, x, ldx, codes, scales, as_stream(stream)));
+}
+
+shampoo4_status shampoo4_fp8_store_weight(shampoo4_dtype dtype, int64_t rows, int64_t cols, const void* w, int64_t ldw,
+                                          uint8_t* codes, uint8_t* scales, uint8_t* t_codes, uint8_t* t_scales,
+                                          void* stream) {
+    CallRange range_("shampoo4_fp8_store_weight");
+    if (!dtype_ok(dtype) || !t_codes != !t_scales) return SHAMPOO4_EINVAL;
+    if (!shape_ok(rows, cols) || (rows + 127) / 128 * ((cols + 127) / 128) >= (int64_t(1) << 24)) return SHAMPOO4_ESHAPE;
+    S4_TRY(matrix_ok(w, dtype, rows, cols, ldw));
+    S4_TRY(fp8_ok(codes, scales, rows));
+    if (t_codes) S4_TRY(fp8_ok(t_codes, t_scales, rows));
+    return launched(launch_fp8_store_weight(dtype, rows, cols, w, ldw, codes, scales, t_codes, t_scales,
+                                            as_stream(stream)));
+}
+
+shampoo4_status shampoo4_fp8_load(shampoo4_dtype dtype, int64_t rows, int64_t cols, int32_t block_rows,
+                                  const uint8_t* codes, const uint8_t* scales, void* x, int64_t ldx, void* stream) {
+    CallRange range_("shampoo4_fp8_load");
+    if (!dtype_ok(dtype) || (block_rows != 1 && block_rows != SHAMPOO4_FP8_BLOCK)) return SHAMPOO4_EINVAL;
+    if (!stream_shape_ok(rows, cols)) return SHAMPOO4_ESHAPE;
+    S4_TRY(matrix_ok(x, dtype, rows, cols, ldx));
+    S4_TRY(fp8_ok(codes, scales, rows));
+    return launched(launch_fp8_load(dtype, rows, cols, block_rows, codes, scales, x, ldx, as_stream(stream)));
+}
+
+size_t shampoo4_fp8_linear_workspace_bytes(shampoo4_dtype out_dtype, int64_t rows, int64_t n, int64_t k,
+                                           int32_t x_quantised) {
+    if (!dtype_ok(out_dtype) || !linear_shape_ok(rows, n, k)) return 0;
+    return linear_workspace_bytes(out_dtype, rows, n, k, x_quantised != 0);
+}
+
+shampoo4_status shampoo4_fp8_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, int64_t rows, int64_t n, int64_t k,
+                                    const void* x, int64_t ldx, const uint8_t* x_codes, const uint8_t* x_scales,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, int32_t accumulate, void* y,
+                                    int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range_("shampoo4_fp8_linear");
+    if (!dtype_ok(dtype) || !dtype_ok(out_dtype) || (x && (x_codes || x_scales))) return SHAMPOO4_EINVAL;
+    if (!linear_shape_ok(rows, n, k)) return SHAMPOO4_ESHAPE;
+    if (x)
+        S4_TRY(matrix_ok(x, dtype, rows, k, ldx));
+    else
+        S4_TRY(fp8_ok(x_codes, x_scales, rows));
+    S4_TRY(fp8_ok(w_codes, w_scales, rows));
+    S4_TRY(matrix_ok(y, out_dtype, rows, n, ldy));
+    S4_TRY(workspace_ok(workspace, workspace_bytes, linear_workspace_bytes(out_dtype, rows, n, k, !x)));
+    const Linear a{x, x_codes, x_scales, w_codes, w_scales, y, rows, n, k, ldx, ldy, accumulate != 0};
+    return launched(launch_linear(dtype, out_dtype, a, workspace, as_stream(stream)));
+}
+
+shampoo4_status shampoo4_dropout(const shampoo4_dropout_config* cfg, shampoo4_dtype dtype, int64_t rows, int64_t cols,
+                                 const void* x, int64_t ldx, void* y, int64_t ldy, void* stream) {
+    CallRange range_("shampoo4_dropout");
+    Drop d;
+    if (!cfg || !dtype_ok(dtype)) return SHAMPOO4_EINVAL;
+    S4_TRY(drop_of(*cfg, d));
+    if (!stream_shape_ok(rows, cols)) return SHAMPOO4_ESHAPE;
+    S4_TRY(matrix_ok(x, dtype, rows, cols, ldx));
+    S4_TRY(matrix_ok(y, dtype, rows, cols, ldy));
+    return launched(launch_dropout(dtype, rows, cols, d, x, ldx, y, ldy, as_stream(stream)));
+}
+
+shampoo4_status shampoo4_block_norm_forward(const shampoo4_block_norm_config* cfg, shampoo4_dtype dtype, int64_t rows,
+                                            int64_t cols, const void* x, int64_t ldx, const void* h, int64_t ldh,
+                                            const float* post_weight, const void* gate, int32_t gate_rows,
+                                            int64_t ldgate, const float* weight, void* out, int64_t ldout, void* y,
+                                            int64_t ldy, uint8_t* y_codes, uint8_t* y_scales, float* h_rstd,
+                                            float* rstd, void* stream) {
+    CallRange range_("shampoo4_block_norm_forward");
+    Drop d;
+    S4_TRY(block_config_ok(cfg));
+    if (!dtype_ok(dtype)) return SHAMPOO4_EINVAL;
+    S4_TRY(drop_of(cfg->dropout, d));
+    if (!block_shape_ok(rows, cols)) return SHAMPOO4_ESHAPE;
+    if (rows == 0) return SHAMPOO4_OK;
+    S4_TRY(matrix_ok(x, dtype, rows, cols, ldx));
+    if (h) {
+        S4_TRY(matrix_ok(h, dtype, rows, cols, ldh));
+        S4_TRY(matrix_ok(out, dtype, rows, cols, ldout));
+        S4_TRY(gate_ok(gate, gate_rows, dtype, rows, cols, ldgate));
+    } else if (post_weight || gate || gate_rows || out || h_rstd || cfg->residual_scale != 1.f) {
+        return SHAMPOO4_EINVAL;
+    }
+    if (!y_codes != !y_scales || (weight ? !y && !y_codes : y || y_codes || rstd)) return SHAMPOO4_EINVAL;
+    if (y) S4_TRY(matrix_ok(y, dtype, rows, cols, ldy));
+    if (y_codes) S4_TRY(fp8_ok(y_codes, y_scales, rows));
+    if (!h && !weight) return SHAMPOO4_EINVAL;
+    if (!aligned(weight, 4) || !aligned(post_weight, 4) || !aligned(rstd, 4) || !aligned(h_rstd, 4)) return SHAMPOO4_EALIGN;
+    const BlockForward a{x, h, post_weight, gate, weight, out, y, y_codes, y_scales, h_rstd, rstd, rows, cols, ldx, ldh,
+                         ldgate, ldout, ldy, cfg->eps, cfg->residual_scale, gate_rows};
+    return launched(launch_block_forward(dtype, a, d, as_stream(stream)));
+}
+
+size_t shampoo4_block_norm_workspace_bytes(int64_t rows, int64_t cols) {
+    return block_shape_ok(rows, cols) ? block_workspace_bytes(rows, cols) : 0;
+}
+
+shampoo4_status shampoo4_block_norm_backward(const shampoo4_block_norm_config* cfg, shampoo4_dtype dtype, int64_t rows,
+                                             int64_t cols, const void* dy, int64_t lddy, const void* dres,
+                                             int64_t lddres, const void* x, int64_t ldx, const float* rstd,
+                                             const float* weight, const void* h, int64_t ldh, const float* h_rstd,
+                                             const float* post_weight, const void* gate, int32_t gate_rows,
+                                             int64_t ldgate, void* dx, int64_t lddx, void* dh, int64_t lddh,
+                                             float* dweight, float* dpost_weight, void* dgate, int64_t lddgate,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    CallRange range_("shampoo4_block_norm_backward");
+    Drop d;
+    S4_TRY(block_config_ok(cfg));
+    if (!dtype_ok(dtype)) return SHAMPOO4_EINVAL;
+    S4_TRY(drop_of(cfg->dropout, d));
+    if (!block_shape_ok(rows, cols)) return SHAMPOO4_ESHAPE;
+    // without a norm before the next block, or without a block, nothing of theirs
+    if (!weight && (dy || rstd || dweight)) return SHAMPOO4_EINVAL;
+    if (rows > 0 && ((weight && (!dy || !rstd || !x)) || (!weight && !dres))) return SHAMPOO4_EINVAL;
+    const bool block = h || rows == 0;
+    if (!block && (post_weight || gate || gate_rows || h_rstd || dh || dpost_weight || dgate || cfg->residual_scale != 1.f))
+        return SHAMPOO4_EINVAL;
+    if (!post_weight && (dpost_weight || h_rstd)) return SHAMPOO4_EINVAL;
+    if (rows > 0 && post_weight && !h_rstd) return SHAMPOO4_EINVAL;
+    if (dgate && !gate && !gate_rows) return SHAMPOO4_EINVAL;
+    if (dy) S4_TRY(matrix_ok(dy, dtype, rows, cols, lddy));
+    if (dres) S4_TRY(matrix_ok(dres, dtype, rows, cols, lddres));
+    if (weight) S4_TRY(matrix_ok(x, dtype, rows, cols, ldx));
+    if (h) S4_TRY(matrix_ok(h, dtype, rows, cols, ldh));
+    S4_TRY(gate_ok(gate, gate_rows, dtype, rows, cols, ldgate));
+    if (dx) S4_TRY(matrix_ok(dx, dtype, rows, cols, lddx));
+    if (dh) S4_TRY(matrix_ok(dh, dtype, rows, cols, lddh));
+    if (dgate) {
+        if (gate_rows)
+            S4_TRY(matrix_ok(dgate, dtype, rows, cols, lddgate));
+        else if (!aligned(dgate, 4))
+            return SHAMPOO4_EALIGN;
+    }
+    if (!aligned(weight, 4) || !aligned(post_weight, 4) || !aligned(rstd, 4) || !aligned(h_rstd, 4) ||
+        !aligned(dweight, 4) || !aligned(dpost_weight, 4))
+        return SHAMPOO4_EALIGN;
+    if (dweight || dpost_weight || (dgate && !gate_rows))
+        S4_TRY(workspace_ok(workspace, workspace_bytes, block_workspace_bytes(rows, cols)));
+    const BlockBackward a{dy, dres, x, h, gate, rstd, weight, h_rstd, post_weight, dx, dh, dgate, dweight, dpost_weight,
+                          (float*)workspace, rows, cols, lddy, lddres, ldx, ldh, ldgate, lddx, lddh, lddgate,
+                          cfg->residual_scale, gate_rows};
+    return launched(launch_block_backward(dtype, a, d, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -103,4 +103,84 @@ struct Policy {
 size_t policy_workspace_bytes(shampoo4_dtype dtype, int64_t rows, int64_t vocab, bool train);
 hipError_t launch_policy(shampoo4_dtype dtype, const Policy& p, void* workspace, hipStream_t stream);
 
+// Calls f(T{}) for an element type.
+template <class F>
+void by_type(shampoo4_dtype dtype, F f) {
+    if (dtype == SHAMPOO4_BF16)
+        f(__bf16{});
+    else if (dtype == SHAMPOO4_F16)
+        f(_Float16{});
+    else
+        f(float{});
+}
+
+// Matrices in e4m3 with a scale for each block of 128 columns.
+hipError_t launch_fp8_store(shampoo4_dtype dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                            uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_fp8_store_weight(shampoo4_dtype dtype, int64_t rows, int64_t cols, const void* w, int64_t ldw,
+                                   uint8_t* codes, uint8_t* scales, uint8_t* t_codes, uint8_t* t_scales,
+                                   hipStream_t stream);
+hipError_t launch_fp8_load(shampoo4_dtype dtype, int64_t rows, int64_t cols, int block_rows, const uint8_t* codes,
+                           const uint8_t* scales, void* x, int64_t ldx, hipStream_t stream);
+
+// Y (+)= X^ W^T.  x NULL: given by its codes and scales.
+struct Linear {
+    const void* x;
+    const uint8_t* xc;
+    const uint8_t* xs;
+    const uint8_t* wc;
+    const uint8_t* ws;
+    void* y;
+    int64_t rows, n, k, ldx, ldy;
+    int accumulate;
+};
+size_t linear_workspace_bytes(shampoo4_dtype out_dtype, int64_t rows, int64_t n, int64_t k, bool x_quantised);
+hipError_t launch_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, const Linear& a, void* workspace,
+                         hipStream_t stream);
+
+struct Drop;                  // random.hpp
+hipError_t launch_dropout(shampoo4_dtype dtype, int64_t rows, int64_t cols, const Drop& d, const void* x, int64_t ldx,
+                          void* y, int64_t ldy, hipStream_t stream);
+
+struct BlockForward {
+    const void* x;
+    const void* h;            // NULL: x' = x, not written
+    const float* post;        // NULL: no norm behind the block
+    const void* gate;         // NULL: 1
+    const float* weight;      // NULL: no y
+    void* out;
+    void* y;                  // NULL: only quantised
+    uint8_t* yc;
+    uint8_t* ys;
+    float* h_rstd;
+    float* rstd;
+    int64_t rows, cols, ldx, ldh, ldgate, ldout, ldy;
+    float eps, rho;
+    int gate_rows;
+};
+hipError_t launch_block_forward(shampoo4_dtype dtype, const BlockForward& a, const Drop& d, hipStream_t stream);
+
+struct BlockBackward {
+    const void* dy;           // NULL with weight NULL
+    const void* dres;         // NULL: 0
+    const void* x;
+    const void* h;            // NULL: no block
+    const void* gate;
+    const float* rstd;
+    const float* weight;
+    const float* h_rstd;
+    const float* post;
+    void* dx;
+    void* dh;
+    void* dgate;
+    float* dweight;
+    float* dpost;
+    float* parts;
+    int64_t rows, cols, lddy, lddres, ldx, ldh, ldgate, lddx, lddh, lddgate;
+    float rho;
+    int gate_rows;
+};
+size_t block_workspace_bytes(int64_t rows, int64_t cols);
+hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& a, const Drop& d, hipStream_t stream);
+
 }  // namespace s4

@@ -254,4 +254,83 @@ __device__ __forceinline__ floatx8 act8_values(u32x2 c, floatx8 s) {
 
 __device__ __forceinline__ u32x2 ldg_u2(const void* p) { return ldg((const u32x2*)p); }
 
+// A finite value beyond float16's range becomes its largest number; NaN passes (both
+// comparisons are false).
+template <class T>
+__device__ __forceinline__ floatx8 saturate(floatx8 f) {
+    if constexpr (__is_same(T, _Float16)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            f[j] = f[j] > 65504.f ? 65504.f : f[j];
+            f[j] = f[j] < -65504.f ? -65504.f : f[j];
+        }
+    }
+    return f;
+}
+
+// -- e4m3 with a scale for each block of 128 columns ---------------------------------------
+
+// Codes' pitch, and that of a row of scales (read four at a time).
+__host__ __device__ constexpr int64_t fp8_pitch(int64_t cols) { return (cols + 127) / 128 * 128; }
+__host__ __device__ constexpr int64_t fp8_scale_pitch(int64_t cols) { return (cols + 511) / 512 * 4; }
+
+// Biased exponent e of a block's scale 2^(e - 127), from the bits of its largest |x|
+// (E + mantissa m): a / 2^(E - 8) = 256 (1 + m) is at most 448 unless m is above 3/4 =
+// 0x600000 / 2^23, where the added 0x1fffff carries into the exponent.
+__device__ __forceinline__ uint32_t fp8_exponent(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return 255u;
+    return (uint32_t)max((int)((amax_bits + 0x1fffffu) >> 23) - 8, 1);
+}
+
+// What codes of a block are made with: 1 / s (x / s is exact, and at most 448), and a mask that is
+// 0 for a block that is not finite.
+struct Fp8Block {
+    float inv;
+    uint32_t mask;
+    __device__ __forceinline__ explicit Fp8Block(uint32_t e)
+        : inv(__uint_as_float((254u - min(e, 253u)) << 23)), mask(e == 255u ? 0u : 0xffffffffu) {}
+    __device__ __forceinline__ u32x2 codes(floatx8 x) const {
+        u32x2 r = {0u, 0u};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            int c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h] * inv, x[4 * h + 1] * inv, 0, false);
+            c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2] * inv, x[4 * h + 3] * inv, c, true);
+            r[h] = (uint32_t)c & mask;
+        }
+        return r;
+    }
+};
+
+// Largest |x| of eight values, as fp32 bits (NaN above infinity).
+__device__ __forceinline__ uint32_t magnitude(floatx8 x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+    return m;
+}
+// The largest over sixteen neighbouring lanes, in each of them.
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xf, 0xf, false));    // row_ror:1
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xf, 0xf, false));    // row_ror:2
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xf, 0xf, false));    // row_ror:4
+    return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xf, 0xf, false)); // row_ror:8
+}
+
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+// Eight codes as numbers (before their scale).
+__device__ __forceinline__ floatx8 fp8_values(u32x2 c) {
+    floatx8 f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const floatx2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], false);
+        const floatx2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)c[h], true);
+        f[4 * h] = a[0];
+        f[4 * h + 1] = a[1];
+        f[4 * h + 2] = b[0];
+        f[4 * h + 3] = b[1];
+    }
+    return f;
+}
+
 }  // namespace s4

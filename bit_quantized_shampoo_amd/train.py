@@ -13,7 +13,8 @@ caller's to order, and to keep, as with any PyTorch operator.
 
 None of these calls is recorded by autograd: an input that requires a gradient is read like
 any other, and the result is detached from it.  Each backward pass is a call of its own
-(activation_backward, act8_weight_grad, embedding_grad, the dlogits of policy_loss).
+(activation_backward, act8_weight_grad, embedding_grad, the dlogits of policy_loss, fp8_linear with
+the transposed weight, block_norm_backward, dropout on the gradient).
 """
 
 from __future__ import annotations
@@ -28,7 +29,8 @@ from . import _lib as L
 _DTYPES = {torch.float32: L.F32, torch.bfloat16: L.BF16, torch.float16: L.F16}
 _KINDS = {"silu": L.ACT_SILU, "gelu": L.ACT_GELU}
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
-_F32, _I8, _U8 = torch.float32, torch.int8, torch.uint8
+_F32, _I8, _U8, _E4M3 = torch.float32, torch.int8, torch.uint8, torch.float8_e4m3fn
+_MASK64 = (1 << 64) - 1
 
 
 def _on_stream(fn):
@@ -458,3 +460,333 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, out: torch.Tenso
     L.check(lib.shampoo4_token_logprobs(dt, _ID_BYTES[targets.dtype], rows, vocab, logits.data_ptr(), ldz, tp, op, wp,
                                         wb, s), "shampoo4_token_logprobs")
     return out
+
+
+# -- products in 8-bit floating point -------------------------------------------------------
+
+class Fp8:
+    """A [rows, cols] matrix in e4m3 with a scale for each block of 128 columns of `block_rows` rows (1:
+    activations, 128: weights): `codes` float8_e4m3fn [rows, P] (P: cols up to a multiple of 128) and
+    `scales` uint8 [rows / block_rows up, S] (S: P / 128 up to a multiple of 4), the value of element
+    (t, c) being codes[t, c] * 2 ** (scales[t // block_rows, c // 128] - 127)."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "block_rows")
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, block_rows: int = 1):
+        if block_rows not in (1, L.FP8_BLOCK):
+            raise ValueError(f"block_rows must be 1 or {L.FP8_BLOCK}, got {block_rows}")
+        shapes = self.padded(rows, cols, block_rows)
+        for t, dtype, want, nm in ((codes, _E4M3, shapes[0], "codes"), (scales, _U8, shapes[1], "scales")):
+            _tensor(t, nm)
+            if t.dtype is not dtype or t.shape != want or not t.is_contiguous():
+                raise ValueError(f"{nm} must be a contiguous {dtype} tensor of shape {want}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales, self.rows, self.cols, self.block_rows = codes, scales, rows, cols, block_rows
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @staticmethod
+    def padded(rows: int, cols: int, block_rows: int = 1):
+        """The shapes of codes and scales."""
+        return (rows, -(-cols // 128) * 128), (-(-rows // block_rows), -(-cols // 512) * 4)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda") -> "Fp8":
+        codes, scales = cls.padded(rows, cols, block_rows)
+        return cls(torch.empty(codes, dtype=_E4M3, device=device), torch.empty(scales, dtype=_U8, device=device), rows,
+                   cols, block_rows)
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def _new_fp8(like: torch.Tensor, rows: int, cols: int, block_rows: int) -> Fp8:
+    a = Fp8.__new__(Fp8)
+    codes, scales = Fp8.padded(rows, cols, block_rows)
+    a.codes, a.scales = like.new_empty(codes, dtype=_E4M3), like.new_empty(scales, dtype=_U8)
+    a.rows, a.cols, a.block_rows = rows, cols, block_rows
+    return a
+
+
+def _fp8(a, what: str, rows, cols, block_rows: int, device):
+    """Checks a quantised matrix (rows or cols None: any) and returns its two pointers."""
+    if not isinstance(a, Fp8):
+        raise TypeError(f"{what} must be an Fp8")
+    if a.block_rows != block_rows:
+        raise ValueError(f"{what} must have blocks of {block_rows} rows, got {a.block_rows}")
+    if (rows is not None and a.rows != rows) or (cols is not None and a.cols != cols):
+        raise ValueError(f"{what} must hold {(rows, cols)}, got {(a.rows, a.cols)}")
+    if a.codes.device != device:
+        raise ValueError(f"{what} must be on {device}, got {a.codes.device}")
+    return a.codes.data_ptr(), a.scales.data_ptr()
+
+
+@_on_stream
+def fp8_store(x: torch.Tensor, out: Fp8 | None = None) -> Fp8:
+    """x in e4m3 with a scale for each 128 columns of a row (an operand of fp8_linear)."""
+    ld = _matrix(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    s = _stream(dev)
+    if out is None:
+        out = _new_fp8(x, rows, cols, 1)
+    c, e = _fp8(out, "out", rows, cols, 1, dev)
+    L.check(L.lib().shampoo4_fp8_store(_DTYPES[x.dtype], rows, cols, x.data_ptr(), ld, c, e, s), "shampoo4_fp8_store")
+    return out
+
+
+@_on_stream
+def fp8_store_weight(w: torch.Tensor, transposed: bool = False, out: Fp8 | None = None, out_t: Fp8 | None = None):
+    """w in e4m3 with a scale for each block of 128 x 128; with transposed=True (w8, wt8), wt8 being w^T
+    in the same codes: fp8_linear(x, w8) is the layer, fp8_linear(dy, wt8) its input's gradient."""
+    ld = _matrix(w, "w")
+    rows, cols = w.shape
+    dev = w.device
+    s = _stream(dev)
+    if out is None:
+        out = _new_fp8(w, rows, cols, L.FP8_BLOCK)
+    c, e = _fp8(out, "out", rows, cols, L.FP8_BLOCK, dev)
+    tc = te = 0
+    if transposed:
+        if out_t is None:
+            out_t = _new_fp8(w, cols, rows, L.FP8_BLOCK)
+        tc, te = _fp8(out_t, "out_t", cols, rows, L.FP8_BLOCK, dev)
+    elif out_t is not None:
+        raise ValueError("out_t needs transposed=True")
+    L.check(L.lib().shampoo4_fp8_store_weight(_DTYPES[w.dtype], rows, cols, w.data_ptr(), ld, c, e, tc, te, s),
+            "shampoo4_fp8_store_weight")
+    return (out, out_t) if transposed else out
+
+
+@_on_stream
+def fp8_load(a: Fp8, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of a quantised matrix, in `dtype` (or in `out`, of its own type)."""
+    if not isinstance(a, Fp8):
+        raise TypeError("a must be an Fp8")
+    rows, cols = a.rows, a.cols
+    dev = a.codes.device
+    s = _stream(dev)
+    if out is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        out = a.codes.new_empty((rows, cols), dtype=dtype)
+        ld = cols
+    else:
+        ld = _matrix(out, "out", None, rows, cols, dev)
+        dtype = out.dtype
+    L.check(L.lib().shampoo4_fp8_load(_DTYPES[dtype], rows, cols, a.block_rows, a.codes.data_ptr(), a.scales.data_ptr(),
+                                      out.data_ptr(), ld, s), "shampoo4_fp8_load")
+    return out
+
+
+@_on_stream
+def fp8_linear(x, w8: Fp8, out: torch.Tensor | None = None, accumulate: bool = False, dtype=None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """x w8^T, [x rows, w8 rows].  x is an Fp8 of fp8_store (or block_norm_forward), or a matrix, which the
+    call quantises in the same way.  The result is of `dtype` (default: x's type, bfloat16 for an Fp8),
+    or goes into `out`, of its own type; accumulate=True adds to `out`.
+
+    A bfloat16 result's products are the 8-bit matrix cores', which cut a term off 13 bits below the largest
+    of its eight neighbours (at most a quarter of bfloat16's rounding); those of a float32 or float16
+    result are exact, with float32 sums, at half the rate."""
+    if isinstance(x, Fp8):
+        rows, k, dev, held = x.rows, x.cols, x.codes.device, x.codes
+        s = _stream(dev)
+        xc, xe = _fp8(x, "x", None, None, 1, dev)
+        xp = ld = 0
+        xdt = torch.bfloat16
+    else:
+        ld = _matrix(x, "x")
+        rows, k = x.shape
+        dev, held, xdt = x.device, x, x.dtype
+        s = _stream(dev)
+        xp, xc, xe = x.data_ptr(), 0, 0
+    wc, we = _fp8(w8, "w8", None, k, L.FP8_BLOCK, dev)
+    n = w8.rows
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        odt = xdt if dtype is None else dtype
+        if odt not in _DTYPES:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {odt}")
+        out = held.new_empty((rows, n), dtype=odt)
+        ldo = n
+    else:
+        ldo = _matrix(out, "out", dtype, rows, n, dev)
+        odt = out.dtype
+    lib = L.lib()
+    o = _DTYPES[odt]
+    ws, wp, wb = _workspace(workspace, lib.shampoo4_fp8_linear_workspace_bytes(o, rows, n, k, not xp), held)
+    L.check(lib.shampoo4_fp8_linear(_DTYPES[xdt], o, rows, n, k, xp, ld, xc, xe, wc, we, int(accumulate), out.data_ptr(),
+                                    ldo, wp, wb, s), "shampoo4_fp8_linear")
+    return out
+
+
+# -- dropout -------------------------------------------------------------------------------
+
+def _dropout_config(p: float, seed: int, offset: int, counter, device) -> L.DropoutConfig:
+    cp = 0
+    if counter is not None:
+        cp = _vector(counter, 1, "counter", torch.int64, device)
+    return L.DropoutConfig(p, 0, seed & _MASK64, offset & _MASK64, cp)
+
+
+@_on_stream
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, counter: torch.Tensor | None = None,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """x with each element dropped with probability p (in steps of 2**-16) and the others divided by what is
+    kept of 1.  Which are dropped follows from (seed, offset + counter, row, column) alone, so that the
+    backward pass is the same call on the gradient, and no mask is stored.  `counter` is an int64 tensor of
+    one element that the kernel reads: a captured graph whose program advances it drops others in each
+    replay.  `out` may be x."""
+    ld = _matrix(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    s = _stream(dev)
+    if out is None:
+        out = x.new_empty((rows, cols))
+        ldo = cols
+    else:
+        ldo = _matrix(out, "out", x.dtype, rows, cols, dev)
+    cfg = _dropout_config(p, seed, offset, counter, dev)
+    L.check(L.lib().shampoo4_dropout(ctypes.byref(cfg), _DTYPES[x.dtype], rows, cols, x.data_ptr(), ld, out.data_ptr(),
+                                     ldo, s), "shampoo4_dropout")
+    return out
+
+
+# -- the ends of a residual block ------------------------------------------------------------
+
+def _gate(gate, dtype, rows: int, cols: int, device, what: str = "gate"):
+    """(pointer, is a matrix, leading dimension) of a gate: float32 [cols], or [rows, cols] of `dtype`."""
+    if gate is None:
+        return 0, 0, 0
+    _tensor(gate, what)
+    if gate.ndim == 1:
+        return _vector(gate, cols, what, _F32, device), 0, 0
+    ld = _matrix(gate, what, dtype, rows, cols, device)
+    return gate.data_ptr(), 1, ld
+
+
+def _out(t, what: str, like: torch.Tensor):
+    """A result's tensor, made where it is not given, and its leading dimension."""
+    rows, cols = like.shape
+    if t is None:
+        return like.new_empty((rows, cols)), cols
+    return t, _matrix(t, what, like.dtype, rows, cols, like.device)
+
+
+@_on_stream
+def block_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                       post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                       residual_scale: float = 1.0, eps: float = 1e-6, p: float = 0.0, seed: int = 0, offset: int = 0,
+                       counter: torch.Tensor | None = None, save8: bool = False, out: torch.Tensor | None = None,
+                       y: torch.Tensor | None = None):
+    """The end of a block and the norm before the next one:
+
+        x' = residual_scale x + gate dropout(h rstd(h) post_weight)
+        y  = x' rstd(x') weight                          rstd(v) = 1 / sqrt(mean(v^2) + eps)
+
+    Returns (x', y, y8, stats): y8 is y quantised as by fp8_store (None without save8), stats is what
+    block_norm_backward needs.  Without `h`, x' is x (the norm alone); without `weight` there is no y;
+    without `post_weight` the block's end is h as it is.  gate: float32 [cols], a matrix like x, or None
+    for 1.  Weights are float32 [cols].  p, seed, offset, counter: as of dropout.  `out` may be x or h."""
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    dev, dtype = x.device, x.dtype
+    s = _stream(dev)
+    hp = ldh = ldo = op = pp = hr = ldy = yp = yc = ye = wp = rr = 0
+    stats = x.new_empty((2, rows), dtype=_F32)
+    gp, grows, ldg = _gate(gate, dtype, rows, cols, dev)
+    if h is not None:
+        ldh = _matrix(h, "h", dtype, rows, cols, dev)
+        hp = h.data_ptr()
+        out, ldo = _out(out, "out", x)
+        op = out.data_ptr()
+        if post_weight is not None:
+            pp = _vector(post_weight, cols, "post_weight", _F32, dev)
+            hr = stats.data_ptr()
+    elif post_weight is not None or gate is not None or out is not None or residual_scale != 1.0:
+        raise ValueError("post_weight, gate, out and residual_scale need h")
+    y8 = None
+    if weight is not None:
+        wp = _vector(weight, cols, "weight", _F32, dev)
+        y, ldy = _out(y, "y", x)
+        yp = y.data_ptr()
+        rr = stats.data_ptr() + 4 * rows
+        if save8:
+            y8 = _new_fp8(x, rows, cols, 1)
+            yc, ye = y8.codes.data_ptr(), y8.scales.data_ptr()
+    elif y is not None or save8 or h is None:
+        raise ValueError("y and save8 need weight, and so does a call without h")
+    cfg = L.BlockNormConfig(eps, residual_scale, _dropout_config(p, seed, offset, counter, dev))
+    L.check(L.lib().shampoo4_block_norm_forward(ctypes.byref(cfg), _DTYPES[dtype], rows, cols, x.data_ptr(), ldx, hp, ldh,
+                                                pp, gp, grows, ldg, wp, op, ldo, yp, ldy, yc, ye, hr, rr, s),
+            "shampoo4_block_norm_forward")
+    return x if h is None else out, y, y8, stats
+
+
+@_on_stream
+def block_norm_backward(dy: torch.Tensor | None, dres: torch.Tensor | None, x: torch.Tensor,
+                        weight: torch.Tensor | None, stats: torch.Tensor, h: torch.Tensor | None = None,
+                        post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                        residual_scale: float = 1.0, eps: float = 1e-6, p: float = 0.0, seed: int = 0,
+                        offset: int = 0, counter: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                        dh: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """(dx, dh, dweight, dpost_weight, dgate) of block_norm_forward, from the gradients of y (`dy`, None without
+    `weight`) and of x' (`dres`, None for 0).  `x` is x', what the forward call returned first; the other
+    arguments are as there.  Gradients of vectors are float32 [cols]; what has no input is None.
+    dx may be dres or dy, and dh may be h or the other of the two."""
+    ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    dev, dtype = x.device, x.dtype
+    s = _stream(dev)
+    ldy = yp = ldr = rp = wp = rr = hp = ldh = hr = pp = ldh2 = dhp = dwp = dpp = dgp = lddg = 0
+    _tensor(stats, "stats")
+    if stats.dtype is not _F32 or stats.shape != (2, rows) or not stats.is_contiguous() or stats.device != dev:
+        raise ValueError(f"stats must be a contiguous float32 tensor of shape {(2, rows)} on {dev}")
+    if dres is not None:
+        ldr = _matrix(dres, "dres", dtype, rows, cols, dev)
+        rp = dres.data_ptr()
+    dweight = dpost = dgate = None
+    if weight is not None:
+        if dy is None:
+            raise ValueError("weight needs dy")
+        ldy = _matrix(dy, "dy", dtype, rows, cols, dev)
+        yp = dy.data_ptr()
+        wp = _vector(weight, cols, "weight", _F32, dev)
+        rr = stats.data_ptr() + 4 * rows
+        dweight = x.new_empty(cols, dtype=_F32)
+        dwp = dweight.data_ptr()
+    elif dy is not None:
+        raise ValueError("dy needs weight")
+    elif dres is None:
+        raise ValueError("one of dy and dres is needed")
+    gp, grows, ldg = _gate(gate, dtype, rows, cols, dev)
+    if h is not None:
+        ldh = _matrix(h, "h", dtype, rows, cols, dev)
+        hp = h.data_ptr()
+        if post_weight is not None:
+            pp = _vector(post_weight, cols, "post_weight", _F32, dev)
+            hr = stats.data_ptr()
+            dpost = x.new_empty(cols, dtype=_F32)
+            dpp = dpost.data_ptr()
+        if gate is not None:
+            dgate, lddg = x.new_empty((rows, cols) if grows else cols, dtype=dtype if grows else _F32), cols
+            dgp = dgate.data_ptr()
+        dh, ldh2 = _out(dh, "dh", x)
+        dhp = dh.data_ptr()
+    elif post_weight is not None or gate is not None or dh is not None or residual_scale != 1.0:
+        raise ValueError("post_weight, gate, dh and residual_scale need h")
+    dx, ldd = _out(dx, "dx", x)
+    lib = L.lib()
+    ws, wsp, wb = _workspace(workspace, lib.shampoo4_block_norm_workspace_bytes(rows, cols), x)
+    cfg = L.BlockNormConfig(eps, residual_scale, _dropout_config(p, seed, offset, counter, dev))
+    L.check(lib.shampoo4_block_norm_backward(ctypes.byref(cfg), _DTYPES[dtype], rows, cols, yp, ldy, rp, ldr,
+                                             x.data_ptr(), ldx, rr, wp, hp, ldh, hr, pp, gp, grows, ldg, dx.data_ptr(),
+                                             ldd, dhp, ldh2, dwp, dpp, dgp, lddg, wsp, wb, s),
+            "shampoo4_block_norm_backward")
+    return dx, dh, dweight, dpost, dgate
