@@ -132,7 +132,258 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(Linear a, uint3
     }
 }
 
+// -- tiles -----------------------------------------------------------------------------------
+
+// Codes of a slice of 64 columns lie in LDS row by row, 64 bytes each, as the loads that go to LDS
+// directly write them: sixteen rows a load, four lanes a row.  The 16-byte quarters of a row change
+// places by its number, so that sixteen rows read at one column cover the 256 bytes of the banks (and
+// eight rows 128); the loading lane takes the quarter that belongs to its place.
+__device__ __forceinline__ int place_of(int row, int quarter) { return quarter ^ (((row >> 1) ^ (row >> 3)) & 3); }
+
+typedef uint32_t Resource __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ Resource resource(const uint8_t* base, int64_t bytes) {
+    const uint64_t p = (uint64_t)base;
+    return Resource{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
+                    (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xffff),
+                    (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)max((int64_t)0, min(bytes, (int64_t)0xfffffff0))),
+                    0x00020000u};
+}
+// 16 (4) bytes a lane from base + voff + soff to LDS at `lds` + 16 (4) lane; zeros past the end.
+// Not known to the compiler as a load, so that its waits for other loads and LDS reads leave these in
+// flight: arrived() waits for them.
+__device__ __forceinline__ void load16_lds(uint32_t lds, Resource r, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r), "s"(soff) : "m0");
+}
+__device__ __forceinline__ void load4_lds(uint32_t lds, Resource r, uint32_t voff, uint32_t soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r), "s"(soff) : "m0");
+}
+// All but the wave's last N loads have arrived and its LDS reads are done, for every wave.
+template <int N>
+__device__ __forceinline__ void arrived() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Operand of 32 rows x 64 columns: 32 codes of row lane % 32, half lane / 32.
+__device__ __forceinline__ Frag read_frag(const uint8_t* lds, int at0, int at1) {
+    return Frag{*(const u32x4*)(lds + at0), *(const u32x4*)(lds + at1)};
+}
+__device__ __forceinline__ bf16x8 widen(u32x4 c, int q) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    union { bf16x2 p[4]; bf16x8 v; } u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        u.p[2 * i] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * q + i], 1.f, false);
+        u.p[2 * i + 1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[2 * q + i], 1.f, true);
+    }
+    return u.v;
+}
+
+// Four waves, 2 x 2, each with T x T blocks of 32 x 32 outputs; four stages of 64 columns.
+template <int T>
+struct TileShape {
+    static constexpr int SIDE = 64 * T;                      // rows of X and of W
+    static constexpr int STAGE = 2 * SIDE * 64;              // bytes: W's rows, then X's
+    static constexpr int LOADS = STAGE / 1024 / 4;           // of a wave, a stage
+    static constexpr int SCALES = 4 * STAGE;                 // behind the stages: two slots of scales
+    static constexpr int SLOT = 2 * 256 * 4;                 // four blocks of k: 256 words of X, 64 of W a wave
+    static constexpr size_t LDS_BYTES = SCALES + 2 * SLOT;
+};
+
+struct TilePlan {
+    int tiles_m, tiles_n, splits;
+    int blocks;               // of k, a range's (a multiple of four)
+};
+
+// Range of k and output tile of this workgroup.  Workgroups go to the eight XCDs round robin; each
+// XCD takes a contiguous range of the tiles (the remainder, under eight, keeps its place), in groups
+// of four tile rows, so that the tiles that one L2 serves share their rows of X and W.
+__device__ __forceinline__ void place(const TilePlan& p, int& split, int& tile_m, int& tile_n) {
+    const int n8 = gridDim.x >> 3;
+    const int b = (int)blockIdx.x < 8 * n8 ? ((int)blockIdx.x & 7) * n8 + ((int)blockIdx.x >> 3) : (int)blockIdx.x;
+    const int tiles = p.tiles_m * p.tiles_n;
+    split = b / tiles;
+    const int t = b - split * tiles;
+    const int g = t / (4 * p.tiles_n);
+    const int gh = min(4, p.tiles_m - 4 * g);
+    const int local = t - 4 * g * p.tiles_n;
+    tile_m = 4 * g + local % gh;
+    tile_n = local / gh;
+}
+
+template <bool EXACT, int T, class O>
+__global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan plan, float* parts) {
+    using S = TileShape<T>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int split, tile_m, tile_n;
+    place(plan, split, tile_m, tile_n);
+    const int64_t m0 = (int64_t)tile_m * S::SIDE, n0 = (int64_t)tile_n * S::SIDE;
+    const int64_t pitch = fp8_pitch(a.k), sp = fp8_scale_pitch(a.k);
+    const int nkb = (int)(pitch >> 7), kb0 = split * plan.blocks, kb1 = min(nkb, kb0 + plan.blocks);
+    const int slices = 2 * (kb1 - kb0);
+    const int wm = (wv & 1) * 32 * T, wn = (wv >> 1) * 32 * T;
+    const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
+
+    // waves 0 and 1 load W's rows, 2 and 3 X's
+    const bool isx = wv >= 2;
+    const int64_t r0 = isx ? m0 : n0, rows = isx ? a.rows : a.n;
+    const Resource codes = resource((isx ? a.xc : a.wc) + r0 * pitch, (rows - r0) * pitch);
+    uint32_t voff[S::LOADS];
+#pragma unroll
+    for (int j = 0; j < S::LOADS; ++j) {
+        const int row = ((wv & 1) * S::LOADS + j) * 16 + (lane >> 2);
+        voff[j] = (uint32_t)(row * pitch + 16 * place_of(row, lane & 3));
+    }
+    const uint32_t to = base + wv * S::LOADS * 1024;
+    const auto load = [&](int s, int j) {
+        const int k = 64 * (2 * kb0 + min(s, slices - 1));   // past the end: the last slice again
+        load16_lds(to + (s & 3) * S::STAGE + j * 1024, codes, voff[j], k);
+    };
+    // scales of four blocks of k: 64 rows of X a wave, and the one row of W's that the wave's outputs take
+    const Resource xscales = resource(a.xs + m0 * sp, (a.rows - m0) * sp);
+    const int64_t wrow = min(n0 + wn, a.n - 1) >> 7;
+    const Resource wscales = resource(a.ws + wrow * sp, ((a.n + 127) / 128 - wrow) * sp);
+    const uint32_t xvoff = (uint32_t)(min(wv * 64 + lane, S::SIDE - 1) * sp);
+    const auto load_scales = [&](int g) {                    // group g of this range
+        const uint32_t k = (uint32_t)min((int64_t)kb0 + 4 * g, sp - 4);
+        const uint32_t slot = base + S::SCALES + (g & 1) * S::SLOT;
+        load4_lds(slot + wv * 256, xscales, xvoff, k);
+        load4_lds(slot + 1024 + wv * 256, wscales, 0, k);
+    };
+
+    floatx16 acc[T][T] = {};                                 // [n][m]: columns of Y in a lane's registers
+    Frag fw[2][T], fx[2][T];
+    uint32_t xe[T], we, xe2[T], we2;
+    const int row = lane & 31, half = lane >> 5;
+    const int at0 = row * 64 + 16 * place_of(row, 2 * half), at1 = row * 64 + 16 * place_of(row, 2 * half + 1);
+    const auto read_part = [&](int s, int i) {               // operand i of W's T and X's T
+        const uint8_t* p = lds + (s & 3) * S::STAGE + (i < T ? wn + 32 * i : S::SIDE + wm + 32 * (i - T)) * 64;
+        (i < T ? fw[s & 1][i % T] : fx[s & 1][i % T]) = read_frag(p, at0, at1);
+    };
+    const auto read_scales = [&](int b, uint32_t (&x)[T], uint32_t& w) {
+        const uint8_t* p = lds + S::SCALES + ((b >> 2) & 1) * S::SLOT + (b & 3);
+#pragma unroll
+        for (int m = 0; m < T; ++m) x[m] = p[(wm + 32 * m + row) * 4];
+        w = p[1024 + wv * 256];
+    };
+    floatx16 part[EXACT ? T : 1][EXACT ? T : 1];
+    const auto products = [&](int f, int n, bool first) {
+#pragma unroll
+        for (int m = 0; m < T; ++m) {
+            if constexpr (!EXACT) {
+                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fw[f][n]), operand(fx[f][m]), acc[n][m], 0,
+                                                                            0, 0, (int)we, 0, (int)xe[m]);
+            } else {
+                floatx16 s = first ? floatx16{} : part[n][m];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(q < 2 ? fw[f][n].lo : fw[f][n].hi, q & 1),
+                                                                widen(q < 2 ? fx[f][m].lo : fx[f][m].hi, q & 1), s, 0, 0, 0);
+                part[n][m] = s;
+                if (!first) {
+                    // the scales' product may leave fp32's range where its product with the sum does not
+                    const int shift = (int)(we + xe[m]) - 254;
+                    const float one = we == 255u || xe[m] == 255u ? __builtin_nanf("") : 1.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[n][m][i] = fmaf(__builtin_amdgcn_ldexpf(s[i], shift), one, acc[n][m][i]);
+                }
+            }
+        }
+    };
+
+    if (slices > 0) {
+        load_scales(0);
+#pragma unroll
+        for (int s = 0; s < 3; ++s)
+#pragma unroll
+            for (int j = 0; j < S::LOADS; ++j) load(s, j);
+        arrived<2 * S::LOADS>();
+#pragma unroll
+        for (int i = 0; i < 2 * T; ++i) read_part(0, i);
+        read_scales(0, xe, we);
+        const auto slice = [&](int s, int f) {
+            // the next slice is whole in LDS, and the stage before this one's is no longer read
+            arrived<S::LOADS>();
+            if (f == 0 && (s & 7) == 0) load_scales((s >> 3) + 1);
+#pragma unroll
+            for (int n = 0; n < T; ++n) {
+                constexpr int PER = (2 * T + T - 1) / T;
+#pragma unroll
+                for (int i = n * PER; i < min(2 * T, (n + 1) * PER); ++i) read_part(s + 1, i);
+#pragma unroll
+                for (int j = n * S::LOADS / T; j < (n + 1) * S::LOADS / T; ++j) load(s + 3, j);
+                if (f == 1 && n == T - 1) read_scales((s + 1) >> 1, xe2, we2);
+                products(f, n, f == 0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        for (int s = 0; s < slices; s += 2) {
+            slice(s, 0);
+            slice(s + 1, 1);
+#pragma unroll
+            for (int m = 0; m < T; ++m) xe[m] = xe2[m];
+            we = we2;
+        }
+        arrived<0>();                                        // nothing is on its way to LDS when the workgroup ends
+    }
+
+    // A lane holds, of row wm + 32 m + lane % 32, columns 8 q + 4 half + 0..3 of each 32 (q = 0..3).
+#pragma unroll
+    for (int m = 0; m < T; ++m) {
+        const int64_t r = m0 + wm + 32 * m + row;
+#pragma unroll
+        for (int n = 0; n < T; ++n)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t col = n0 + wn + 32 * n + 8 * q + 4 * half;
+                if (r >= a.rows || col >= a.n) continue;
+                const floatx4 v = {acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
+                const int k = (int)min((int64_t)4, a.n - col);
+                if (parts)
+                    put4(parts + ((int64_t)split * a.rows + r) * a.n + col, v, k, false);
+                else
+                    put4((O*)a.y + r * a.ldy + col, v, k, a.accumulate != 0);
+            }
+    }
+}
+
+// Y (+)= the ranges' sums, in order.
+template <class O>
+__global__ __launch_bounds__(256) void linear_join_kernel(Linear a, const float* parts, int splits) {
+    const int64_t count = a.rows * a.n;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
+        float s = ldg(parts + i);
+        for (int k = 1; k < splits; ++k) s += ldg(parts + k * count + i);
+        O* p = (O*)a.y + i / a.n * a.ldy + i % a.n;
+        stg(p, (O)(a.accumulate ? (float)ldg(p) + s : s));
+    }
+}
+
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
+
+// How a product is done: by rows of X and 16 columns of Y a workgroup, or by tiles.
+enum class Way { ROWS, TILE128, TILE256 };
+struct LinearPlan {
+    Way way;
+    TilePlan tile;
+};
+LinearPlan linear_plan(bool exact, int64_t rows, int64_t n, int64_t k) {
+    LinearPlan p{};
+    p.way = Way::ROWS;
+    const int64_t pitch = fp8_pitch(k);
+    if (rows <= 64 || pitch > (1 << 23)) return p;
+    const int nkb = (int)(pitch >> 7);
+    const auto tiles = [&](int side) { return ((rows + side - 1) / side) * ((n + side - 1) / side); };
+    const int side = !exact && tiles(256) >= 192 ? 256 : 128;
+    p.way = side == 256 ? Way::TILE256 : Way::TILE128;
+    p.tile.tiles_m = (int)((rows + side - 1) / side);
+    p.tile.tiles_n = (int)((n + side - 1) / side);
+    int splits = 1;
+    while (side == 128 && splits < 16 && tiles(128) * splits * 2 <= 512 && nkb >= 8 * splits) splits *= 2;
+    p.tile.blocks = ((nkb + splits - 1) / splits + 3) / 4 * 4;
+    p.tile.splits = (nkb + p.tile.blocks - 1) / p.tile.blocks;
+    return p;
+}
 
 template <class X, class O>
 hipError_t launch_rows(const Linear& a, hipStream_t stream) {
@@ -146,33 +397,66 @@ hipError_t launch_rows(const Linear& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <bool EXACT, int T, class O>
+hipError_t launch_tiles(const Linear& a, const TilePlan& p, float* parts, hipStream_t stream) {
+    using S = TileShape<T>;
+    static const hipError_t attr = hipFuncSetAttribute((const void*)linear_tile_kernel<EXACT, T, O>,
+                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS_BYTES);
+    if (attr != hipSuccess) return attr;
+    S4_LAUNCH((linear_tile_kernel<EXACT, T, O>), dim3((uint32_t)(p.tiles_m * p.tiles_n * p.splits)), dim3(256),
+              S::LDS_BYTES, stream, a, p, p.splits > 1 ? parts : nullptr);
+    if (p.splits > 1) {
+        const dim3 grid((uint32_t)std::min<int64_t>((a.rows * a.n + 255) / 256, 4096));
+        S4_LAUNCH(linear_join_kernel<O>, grid, dim3(256), 0, stream, a, (const float*)parts, p.splits);
+    }
+    return hipGetLastError();
+}
+
+// X is quantised into the workspace, unless it is quantised already or its few rows are within the product.
+bool quantise_first(const LinearPlan& p, int64_t rows, bool x_quantised) {
+    return !x_quantised && (p.way != Way::ROWS || rows > 16);
+}
+
 }  // namespace
 
 size_t linear_workspace_bytes(shampoo4_dtype out_dtype, int64_t rows, int64_t n, int64_t k, bool x_quantised) {
-    if (rows <= 16 || x_quantised) return 0;
-    return up256((size_t)(rows * fp8_pitch(k))) + up256((size_t)(rows * fp8_scale_pitch(k)));
+    const LinearPlan p = linear_plan(out_dtype != SHAMPOO4_BF16, rows, n, k);
+    size_t bytes = 0;
+    if (quantise_first(p, rows, x_quantised))
+        bytes = up256((size_t)(rows * fp8_pitch(k))) + up256((size_t)(rows * fp8_scale_pitch(k)));
+    if (p.way != Way::ROWS && p.tile.splits > 1) bytes += up256((size_t)p.tile.splits * rows * n * 4);
+    return bytes;
 }
 
 hipError_t launch_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, const Linear& given, void* workspace,
                          hipStream_t stream) {
     if (given.rows <= 0) return hipSuccess;
     Linear a = given;
-    if (a.x && a.rows > 16) {
-        uint8_t* codes = (uint8_t*)workspace;
-        uint8_t* scales = codes + up256((size_t)(a.rows * fp8_pitch(a.k)));
-        const hipError_t e = launch_fp8_store(dtype, a.rows, a.k, a.x, a.ldx, codes, scales, stream);
+    const LinearPlan p = linear_plan(out_dtype != SHAMPOO4_BF16, a.rows, a.n, a.k);
+    uint8_t* ws = (uint8_t*)workspace;
+    if (quantise_first(p, a.rows, !a.x)) {
+        uint8_t* scales = ws + up256((size_t)(a.rows * fp8_pitch(a.k)));
+        const hipError_t e = launch_fp8_store(dtype, a.rows, a.k, a.x, a.ldx, ws, scales, stream);
         if (e != hipSuccess) return e;
         a.x = nullptr;
-        a.xc = codes;
+        a.xc = ws;
         a.xs = scales;
+        ws = scales + up256((size_t)(a.rows * fp8_scale_pitch(a.k)));
     }
     hipError_t e = hipSuccess;
     by_type(out_dtype, [&](auto o) {
         using O = decltype(o);
-        if (!a.x)
-            e = launch_rows<uint8_t, O>(a, stream);
-        else
-            by_type(dtype, [&](auto x) { e = launch_rows<decltype(x), O>(a, stream); });
+        constexpr bool EXACT = !std::is_same_v<O, __bf16>;
+        if (p.way == Way::ROWS) {
+            if (!a.x)
+                e = launch_rows<uint8_t, O>(a, stream);
+            else
+                by_type(dtype, [&](auto x) { e = launch_rows<decltype(x), O>(a, stream); });
+        } else if (p.way == Way::TILE128) {
+            e = launch_tiles<EXACT, 2, O>(a, p.tile, (float*)ws, stream);
+        } else if constexpr (!EXACT) {
+            e = launch_tiles<false, 4, O>(a, p.tile, (float*)ws, stream);
+        }
     });
     return e;
 }

@@ -101,11 +101,14 @@ bool stream_shape_ok(int64_t rows, int64_t cols) {
 
 bool linear_shape_ok(int64_t rows, int64_t n, int64_t k) {
     return shape_ok(rows, n) && k >= 1 && k <= kMaxDim &&
-           ((rows + 63) / 64) * ((n + 63) / 64) < (int64_t(1) << 22) && stream_shape_ok(rows, k);
+           // 64 x 16 outputs and 512 threads a workgroup
+           ((rows + 63) / 64) * ((n + 15) / 16) < (int64_t(1) << 23) && stream_shape_ok(rows, k);
 }
 
 bool block_shape_ok(int64_t rows, int64_t cols) {
-    return rows >= 0 && rows < (int64_t(1) << 24) && cols >= 1 && cols <= SHAMPOO4_BLOCK_NORM_COLS;
+    // a row takes up to 256 threads, 512 from 4097 columns on, 1024 from 8193 on
+    const int64_t most = int64_t(1) << (cols > 8192 ? 22 : cols > 4096 ? 23 : 24);
+    return rows >= 0 && rows < most && cols >= 1 && cols <= SHAMPOO4_BLOCK_NORM_COLS;
 }
 
 shampoo4_status drop_of(const shampoo4_dropout_config& c, Drop& d) {

@@ -282,19 +282,22 @@ __device__ __forceinline__ uint32_t fp8_exponent(uint32_t amax_bits) {
     return (uint32_t)max((int)((amax_bits + 0x1fffffu) >> 23) - 8, 1);
 }
 
-// What codes of a block are made with: 1 / s (x / s is exact, and at most 448), and a mask that is
-// 0 for a block that is not finite.
+// What codes of a block are made with: 1 / s (x / s is exact), the largest |x / s| that is kept
+// (240 where 256 s is 2^128, so that a code times s is finite), and a mask that is 0 for a block
+// that is not finite.
 struct Fp8Block {
-    float inv;
+    float inv, top;
     uint32_t mask;
     __device__ __forceinline__ explicit Fp8Block(uint32_t e)
-        : inv(__uint_as_float((254u - min(e, 253u)) << 23)), mask(e == 255u ? 0u : 0xffffffffu) {}
+        : inv(__uint_as_float((254u - min(e, 253u)) << 23)), top(e >= 247u ? 240.f : 448.f),
+          mask(e == 255u ? 0u : 0xffffffffu) {}
+    __device__ __forceinline__ float scaled(float x) const { return __builtin_amdgcn_fmed3f(x * inv, -top, top); }
     __device__ __forceinline__ u32x2 codes(floatx8 x) const {
         u32x2 r = {0u, 0u};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            int c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h] * inv, x[4 * h + 1] * inv, 0, false);
-            c = __builtin_amdgcn_cvt_pk_fp8_f32(x[4 * h + 2] * inv, x[4 * h + 3] * inv, c, true);
+            int c = __builtin_amdgcn_cvt_pk_fp8_f32(scaled(x[4 * h]), scaled(x[4 * h + 1]), 0, false);
+            c = __builtin_amdgcn_cvt_pk_fp8_f32(scaled(x[4 * h + 2]), scaled(x[4 * h + 3]), c, true);
             r[h] = (uint32_t)c & mask;
         }
         return r;

@@ -194,8 +194,9 @@ SHAMPOO4_API shampoo4_status shampoo4_token_logprobs(shampoo4_dtype dtype, int32
  * A block is 128 columns of 1 row (block_rows = 1: activations and their gradients) or of 128
  * rows (block_rows = 128: weights).  With a = max |x| over the block, its scale is the power of
  * two s = 2^(e - 127), e the smallest value in [1, 254] with a / s <= 448, and a code is x / s
- * rounded to the nearest e4m3 number (ties to even).  A block that holds an infinity or NaN
- * has e = 255 and codes 0, and stands for NaN.
+ * rounded to the nearest e4m3 number (ties to even).  (Where 256 s is 2^128, |x / s| stops at 240,
+ * so that the restored value is finite.)  A block that holds an infinity or NaN has e = 255 and
+ * codes 0, and stands for NaN.
  *
  * A scale that is a power of two is an operand of this GPU's scaled matrix instructions, and
  * a weight's block is square, so that the transposed weight has the same codes and scales.
@@ -246,7 +247,8 @@ SHAMPOO4_API shampoo4_status shampoo4_fp8_load(shampoo4_dtype dtype, int64_t row
  *
  * k >= 1 and n >= 1; rows = 0: nothing is done.  The workspace (NULL when the size is 0) holds
  * the quantised x and partial sums of ranges of k.  Y must overlap nothing else.
- * ESHAPE: rows, n or k above 2^31 - 64, or from 2^22 tiles of 64 x 64 outputs on. */
+ * ESHAPE: rows, n or k above 2^31 - 64, from 2^23 tiles of 64 rows x 16 columns of Y on, or an X
+ * that shampoo4_fp8_store refuses. */
 SHAMPOO4_API size_t shampoo4_fp8_linear_workspace_bytes(shampoo4_dtype out_dtype, int64_t rows, int64_t n, int64_t k,
                                                         int32_t x_quantised);
 SHAMPOO4_API shampoo4_status shampoo4_fp8_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, int64_t rows, int64_t n,
@@ -295,7 +297,7 @@ SHAMPOO4_API shampoo4_status shampoo4_dropout(const shampoo4_dropout_config* cfg
  * and h_rstd NULL.  out may be x or h itself, and y may be h, each with its leading dimension.
  * eps: at least 1e-30, finite.  Finite rows of any size have their norm (squares beyond fp32 are taken
  * of the row divided by a power of two).
- * ESHAPE: cols above 16384, or 2^24 rows or more. */
+ * ESHAPE: cols above 16384, or 2^24 rows or more (2^23 from 4097 columns on, 2^22 from 8193 on). */
 #define SHAMPOO4_BLOCK_NORM_COLS 16384
 typedef struct {
     float eps, residual_scale;

@@ -179,7 +179,8 @@ def fp8_store(x, block_rows=1):
                 continue
             k = fp8_scale_exponent(float(np.max(np.abs(blk))))
             scales[b, j] = k + 127
-            codes[rows, cols] = e4m3_code(blk / 2.0 ** k)
+            top = 240 if 256.0 * 2.0 ** k >= 2.0 ** 128 else 448
+            codes[rows, cols] = e4m3_code(np.clip(blk / 2.0 ** k, -top, top))
     return codes, scales
 
 
