@@ -59,6 +59,13 @@ __device__ __forceinline__ void put4(O* p, floatx4 v, int n, bool accumulate) {
         if (i < n) stg(p + i, (O)(accumulate ? (float)ldg(p + i) + v[i] : v[i]));
 }
 
+// Columns col .. col + 7 of a row of Y, of which k exist.
+template <class O>
+__device__ __forceinline__ void put8(O* row, int64_t col, int64_t cols, floatx8 v, int k, bool accumulate) {
+    if (accumulate) v += Vec8<O>::get(k == 8 ? load8(row + col) : load8_edge(row, col, cols));
+    store8_n(row + col, Vec8<O>::put(v), k);
+}
+
 // X's element type as a kernel's parameter: uint8_t where it is given as codes.
 constexpr int WAVES = 8;
 
@@ -134,11 +141,12 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(Linear a, uint3
 
 // -- tiles -----------------------------------------------------------------------------------
 
-// Codes of a slice of 64 columns lie in LDS row by row, 64 bytes each, as the loads that go to LDS
-// directly write them: sixteen rows a load, four lanes a row.  The 16-byte quarters of a row change
-// places by its number, so that sixteen rows read at one column cover the 256 bytes of the banks (and
-// eight rows 128); the loading lane takes the quarter that belongs to its place.
-__device__ __forceinline__ int place_of(int row, int quarter) { return quarter ^ (((row >> 1) ^ (row >> 3)) & 3); }
+// Codes of a block of 128 columns lie in LDS row by row, as the loads that go to LDS directly write
+// them: eight rows a load, eight lanes a row (whole lines of 128 bytes: of halves of lines, L2 serves
+// only as many).  The 16-byte pieces of a row change places by its number, so that the lanes that LDS
+// serves at once cover the 256 bytes of its banks; the loading lane takes the piece that belongs to its
+// place.
+__device__ __forceinline__ int place_of(int row, int piece) { return piece ^ ((row >> 1) & 7); }
 
 typedef uint32_t Resource __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ Resource resource(const uint8_t* base, int64_t bytes) {
@@ -152,21 +160,20 @@ __device__ __forceinline__ Resource resource(const uint8_t* base, int64_t bytes)
 // Not known to the compiler as a load, so that its waits for other loads and LDS reads leave these in
 // flight: arrived() waits for them.
 __device__ __forceinline__ void load16_lds(uint32_t lds, Resource r, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r), "s"(soff) : "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r), "s"(soff));
 }
 __device__ __forceinline__ void load4_lds(uint32_t lds, Resource r, uint32_t voff, uint32_t soff) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r), "s"(soff) : "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds" ::"s"(lds), "v"(voff), "s"(r), "s"(soff));
 }
 // All but the wave's last N loads have arrived and its LDS reads are done, for every wave.
 template <int N>
 __device__ __forceinline__ void arrived() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
+// The wave's LDS reads are done, for every wave.
+__device__ __forceinline__ void all_read() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// Operand of 32 rows x 64 columns: 32 codes of row lane % 32, half lane / 32.
-__device__ __forceinline__ Frag read_frag(const uint8_t* lds, int at0, int at1) {
-    return Frag{*(const u32x4*)(lds + at0), *(const u32x4*)(lds + at1)};
-}
+// Eight of a lane's codes as an operand of the bf16 matrix cores.
 __device__ __forceinline__ bf16x8 widen(u32x4 c, int q) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     union { bf16x2 p[4]; bf16x8 v; } u;
@@ -178,15 +185,17 @@ __device__ __forceinline__ bf16x8 widen(u32x4 c, int q) {
     return u.v;
 }
 
-// Four waves, 2 x 2, each with T x T blocks of 32 x 32 outputs; four stages of 64 columns.
+// Four waves, 2 x 2, each with T x T blocks of 16 x 16 outputs; two stages of a block of k.
 template <int T>
 struct TileShape {
-    static constexpr int SIDE = 64 * T;                      // rows of X and of W
-    static constexpr int STAGE = 2 * SIDE * 64;              // bytes: W's rows, then X's
-    static constexpr int LOADS = STAGE / 1024 / 4;           // of a wave, a stage
+    static constexpr int SIDE = 32 * T;                      // rows of X, and of W
+    static constexpr int STAGE = SIDE * 128;                 // bytes: of W's rows (two stages), and of X's behind them
+    static constexpr int LOADS = 2 * STAGE / 1024 / 4;       // of a wave, a stage
+    static constexpr int X = 2 * STAGE;
     static constexpr int SCALES = 4 * STAGE;                 // behind the stages: two slots of scales
-    static constexpr int SLOT = 2 * 256 * 4;                 // four blocks of k: 256 words of X, 64 of W a wave
+    static constexpr int SLOT = 2 * 4 * 256;                 // four blocks of k: 64 words of X and of W a wave
     static constexpr size_t LDS_BYTES = SCALES + 2 * SLOT;
+    static_assert(SIDE <= 256 && 128 % (16 * T) == 0, "a lane's row of X for scales, one scale of W a wave");
 };
 
 struct TilePlan {
@@ -220,130 +229,167 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
     const int64_t m0 = (int64_t)tile_m * S::SIDE, n0 = (int64_t)tile_n * S::SIDE;
     const int64_t pitch = fp8_pitch(a.k), sp = fp8_scale_pitch(a.k);
     const int nkb = (int)(pitch >> 7), kb0 = split * plan.blocks, kb1 = min(nkb, kb0 + plan.blocks);
-    const int slices = 2 * (kb1 - kb0);
-    const int wm = (wv & 1) * 32 * T, wn = (wv >> 1) * 32 * T;
+    const int wm = (wv & 1) * 16 * T, wn = (wv >> 1) * 16 * T;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
     // waves 0 and 1 load W's rows, 2 and 3 X's
     const bool isx = wv >= 2;
     const int64_t r0 = isx ? m0 : n0, rows = isx ? a.rows : a.n;
-    const Resource codes = resource((isx ? a.xc : a.wc) + r0 * pitch, (rows - r0) * pitch);
-    uint32_t voff[S::LOADS];
-#pragma unroll
-    for (int j = 0; j < S::LOADS; ++j) {
-        const int row = ((wv & 1) * S::LOADS + j) * 16 + (lane >> 2);
-        voff[j] = (uint32_t)(row * pitch + 16 * place_of(row, lane & 3));
-    }
-    const uint32_t to = base + wv * S::LOADS * 1024;
-    const auto load = [&](int s, int j) {
-        const int k = 64 * (2 * kb0 + min(s, slices - 1));   // past the end: the last slice again
-        load16_lds(to + (s & 3) * S::STAGE + j * 1024, codes, voff[j], k);
+    const Resource codes = resource((isx ? a.xc : a.wc) + r0 * pitch, min(rows - r0, (int64_t)S::SIDE) * pitch);   // at most 2^31 bytes
+    const int lrow = (wv & 1) * S::LOADS * 8 + (lane >> 3);
+    const uint32_t even = (uint32_t)(lrow * pitch + 16 * place_of(lrow, lane & 7));
+    const uint32_t odd = (uint32_t)(lrow * pitch + 16 * place_of(lrow + 8, lane & 7));
+    const uint32_t to = base + (isx ? S::X : 0) + (wv & 1) * S::LOADS * 1024;
+    uint32_t rows8 = (uint32_t)(8 * pitch);
+    const auto load = [&](int b, int stage, int j) {         // past the last block: zeros, by an offset past the end
+        asm volatile("" : "+s"(rows8));                      // added here, not kept in a register for each j
+        const uint32_t v = (j & 1 ? odd : even) + (j * rows8 + (b < kb1 ? 0u : 0x80000000u));
+        load16_lds(to + (stage & 1) * S::STAGE + j * 1024, codes, v, b < kb1 ? 128 * b : 0);
     };
     // scales of four blocks of k: 64 rows of X a wave, and the one row of W's that the wave's outputs take
     const Resource xscales = resource(a.xs + m0 * sp, (a.rows - m0) * sp);
     const int64_t wrow = min(n0 + wn, a.n - 1) >> 7;
     const Resource wscales = resource(a.ws + wrow * sp, ((a.n + 127) / 128 - wrow) * sp);
     const uint32_t xvoff = (uint32_t)(min(wv * 64 + lane, S::SIDE - 1) * sp);
-    const auto load_scales = [&](int g) {                    // group g of this range
-        const uint32_t k = (uint32_t)min((int64_t)kb0 + 4 * g, sp - 4);
-        const uint32_t slot = base + S::SCALES + (g & 1) * S::SLOT;
+    const auto load_scales = [&](int b) {                    // of block b (a multiple of four) and the three after it
+        const uint32_t k = (uint32_t)min((int64_t)b, sp - 4);
+        const uint32_t slot = base + S::SCALES + ((b >> 2) & 1) * S::SLOT;
         load4_lds(slot + wv * 256, xscales, xvoff, k);
-        load4_lds(slot + 1024 + wv * 256, wscales, 0, k);
+        load4_lds(slot + S::SLOT / 2 + wv * 256, wscales, 0, k);
     };
 
-    floatx16 acc[T][T] = {};                                 // [n][m]: columns of Y in a lane's registers
-    Frag fw[2][T], fx[2][T];
-    uint32_t xe[T], we, xe2[T], we2;
-    const int row = lane & 31, half = lane >> 5;
-    const int at0 = row * 64 + 16 * place_of(row, 2 * half), at1 = row * 64 + 16 * place_of(row, 2 * half + 1);
-    const auto read_part = [&](int s, int i) {               // operand i of W's T and X's T
-        const uint8_t* p = lds + (s & 3) * S::STAGE + (i < T ? wn + 32 * i : S::SIDE + wm + 32 * (i - T)) * 64;
-        (i < T ? fw[s & 1][i % T] : fx[s & 1][i % T]) = read_frag(p, at0, at1);
+    // A block is two halves, of X's first and last T / 2 operands with all of W's.
+    floatx4 acc[T][T] = {};                                  // [n][m]: columns of Y in a lane's registers
+    Frag fw[2][T], fx[T];                                    // W's: of this block and of the next
+    uint32_t xe[T], we[2];
+    const int row = lane & 15;
+    const int at0 = row * 128 + 16 * place_of(row, lane >> 4), at1 = row * 128 + 16 * place_of(row, 4 + (lane >> 4));
+    const auto frag = [&](const uint8_t* p, int stage, int i) {
+        const int at = (stage & 1) * S::STAGE + i * 16 * 128;
+        return Frag{*(const u32x4*)(p + at0 + at), *(const u32x4*)(p + at1 + at)};
     };
-    const auto read_scales = [&](int b, uint32_t (&x)[T], uint32_t& w) {
-        const uint8_t* p = lds + S::SCALES + ((b >> 2) & 1) * S::SLOT + (b & 3);
+    const auto read_x = [&](int stage, int m) { fx[m] = frag(lds + S::X + wm * 128, stage, m); };
+    const auto read_w = [&](int stage, int n) { fw[stage & 1][n] = frag(lds + wn * 128, stage, n); };
+    const auto scale_slot = [&](int b) { return lds + S::SCALES + ((b >> 2) & 1) * S::SLOT + (b & 3); };
+    const auto read_xe = [&](int b, int m) { xe[m] = scale_slot(b)[(wm + 16 * m + row) * 4]; };
+    const auto read_we = [&](int b, int stage) { we[stage & 1] = scale_slot(b)[S::SLOT / 2 + wv * 256]; };
+    const auto product = [&](int stage, int n, int m) {
+        const Frag &w = fw[stage & 1][n], &x = fx[m];
+        if constexpr (!EXACT) {
+            // as written: left to itself the compiler finds no place for these sums and operands in 512 registers
+            asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
+                         : "+a"(acc[n][m])
+                         : "v"(operand(w)), "v"(operand(x)), "v"(we[stage & 1]), "v"(xe[m]));
+        } else {
+            floatx4 s = {};
 #pragma unroll
-        for (int m = 0; m < T; ++m) x[m] = p[(wm + 32 * m + row) * 4];
-        w = p[1024 + wv * 256];
-    };
-    floatx16 part[EXACT ? T : 1][EXACT ? T : 1];
-    const auto products = [&](int f, int n, bool first) {
+            for (int q = 0; q < 4; ++q)
+                s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(q < 2 ? w.lo : w.hi, q & 1), widen(q < 2 ? x.lo : x.hi, q & 1),
+                                                            s, 0, 0, 0);
+            // the scales' product may leave fp32's range where its product with the sum does not
+            const int shift = (int)(we[stage & 1] + xe[m]) - 254;
+            const float one = we[stage & 1] == 255u || xe[m] == 255u ? __builtin_nanf("") : 1.f;
 #pragma unroll
-        for (int m = 0; m < T; ++m) {
-            if constexpr (!EXACT) {
-                acc[n][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fw[f][n]), operand(fx[f][m]), acc[n][m], 0,
-                                                                            0, 0, (int)we, 0, (int)xe[m]);
-            } else {
-                floatx16 s = first ? floatx16{} : part[n][m];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(widen(q < 2 ? fw[f][n].lo : fw[f][n].hi, q & 1),
-                                                                widen(q < 2 ? fx[f][m].lo : fx[f][m].hi, q & 1), s, 0, 0, 0);
-                part[n][m] = s;
-                if (!first) {
-                    // the scales' product may leave fp32's range where its product with the sum does not
-                    const int shift = (int)(we + xe[m]) - 254;
-                    const float one = we == 255u || xe[m] == 255u ? __builtin_nanf("") : 1.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[n][m][i] = fmaf(__builtin_amdgcn_ldexpf(s[i], shift), one, acc[n][m][i]);
-                }
-            }
+            for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(__builtin_amdgcn_ldexpf(s[i], shift), one, acc[n][m][i]);
         }
     };
 
-    if (slices > 0) {
-        load_scales(0);
+    if (kb0 < kb1) {
+        load_scales(kb0);
 #pragma unroll
-        for (int s = 0; s < 3; ++s)
+        for (int j = 0; j < S::LOADS; ++j) load(kb0, 0, j);
 #pragma unroll
-            for (int j = 0; j < S::LOADS; ++j) load(s, j);
-        arrived<2 * S::LOADS>();
+        for (int j = 0; j < S::LOADS; ++j) load(kb0 + 1, 1, j);
+        arrived<S::LOADS>();
 #pragma unroll
-        for (int i = 0; i < 2 * T; ++i) read_part(0, i);
-        read_scales(0, xe, we);
-        const auto slice = [&](int s, int f) {
-            // the next slice is whole in LDS, and the stage before this one's is no longer read
-            arrived<S::LOADS>();
-            if (f == 0 && (s & 7) == 0) load_scales((s >> 3) + 1);
+        for (int n = 0; n < T; ++n) read_w(0, n);
+        read_we(kb0, 0);
 #pragma unroll
-            for (int n = 0; n < T; ++n) {
-                constexpr int PER = (2 * T + T - 1) / T;
+        for (int m = 0; m < T / 2; ++m) {
+            read_x(0, m);
+            read_xe(kb0, m);
+        }
+        // Beside the first products of a block the rest of its operands are read; then its place in LDS is free, and
+        // the loads of the block after the next are spread over the products that follow: a CU takes one in
+        // 16 clocks at best (one in 22 when all of them load), and a wave that waits to issue one issues no
+        // product.  Beside the second half the next block's first operands are read.
+        constexpr int STEPS = T * T / 2, FREE = STEPS * 3 / 8, SPREAD = 2 * STEPS - FREE;
+        constexpr int EARLY = ((STEPS - FREE) * S::LOADS + SPREAD - 1) / SPREAD;     // loads of the first half
+        constexpr int NEXT = (3 * T / 2 + STEPS - 1) / STEPS;                        // operands read a step
+        const auto load_step = [&](int b, int stage, int k) {
 #pragma unroll
-                for (int i = n * PER; i < min(2 * T, (n + 1) * PER); ++i) read_part(s + 1, i);
+            for (int j = 0; j < S::LOADS; ++j)
+                if (FREE + j * SPREAD / S::LOADS == k) load(b, stage, j);
+        };
+        // Block b, in stage J = b % 2.  Beside an even one the scales of the next four blocks are loaded (twice, as
+        // that takes no branch: over one the compiler moves products past the barriers that they are to cover).
+        const auto block = [&](int b, auto j) {
+            constexpr int J = decltype(j)::value;
 #pragma unroll
-                for (int j = n * S::LOADS / T; j < (n + 1) * S::LOADS / T; ++j) load(s + 3, j);
-                if (f == 1 && n == T - 1) read_scales((s + 1) >> 1, xe2, we2);
-                products(f, n, f == 0);
+            for (int k = 0; k < STEPS; ++k) {
+                if (k < T / 2) {
+                    read_x(J, T / 2 + k);
+                    read_xe(b, T / 2 + k);
+                }
+                if (k == FREE) {
+                    all_read();
+                    if (J == 0) load_scales((b & ~3) + 4);
+                }
+                load_step(b + 2, J, k);
+                product(J, k % T, k / T);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            // the next block is whole in LDS; only what has just been issued is on its way
+            arrived<EARLY + (J == 0 ? 2 : 0)>();
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+#pragma unroll
+                for (int i = k * NEXT; i < (k + 1) * NEXT; ++i) {
+                    if (i == 0) read_we(b + 1, J + 1);
+                    if (i < T) read_w(J + 1, i);
+                    if (i >= T && i < 3 * T / 2) {
+                        read_x(J + 1, i - T);
+                        read_xe(b + 1, i - T);
+                    }
+                }
+                load_step(b + 2, J, STEPS + k);
+                product(J, k % T, T / 2 + k / T);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        for (int s = 0; s < slices; s += 2) {
-            slice(s, 0);
-            slice(s + 1, 1);
-#pragma unroll
-            for (int m = 0; m < T; ++m) xe[m] = xe2[m];
-            we = we2;
+        // An odd number of blocks is made even: codes past the last one are 0, and their scales padding.
+        for (int b = kb0; b < kb1; b += 2) {
+            block(b, std::integral_constant<int, 0>{});
+            block(b + 1, std::integral_constant<int, 1>{});
         }
         arrived<0>();                                        // nothing is on its way to LDS when the workgroup ends
+        asm volatile("s_nop 15\n\ts_nop 15");                // and the last sums are written
     }
 
-    // A lane holds, of row wm + 32 m + lane % 32, columns 8 q + 4 half + 0..3 of each 32 (q = 0..3).
+    // A lane holds, of row wm + 16 m + lane % 16, columns 4 (lane / 16) + 0..3 of each 16; two exchanges of lanes
+    // give it eight neighbouring columns of each 32.
 #pragma unroll
     for (int m = 0; m < T; ++m) {
-        const int64_t r = m0 + wm + 32 * m + row;
+        const int64_t r = m0 + wm + 16 * m + row;
 #pragma unroll
-        for (int n = 0; n < T; ++n)
+        for (int n = 0; n < T; n += 2) {
+            floatx8 v;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t col = n0 + wn + 32 * n + 8 * q + 4 * half;
-                if (r >= a.rows || col >= a.n) continue;
-                const floatx4 v = {acc[n][m][4 * q], acc[n][m][4 * q + 1], acc[n][m][4 * q + 2], acc[n][m][4 * q + 3]};
-                const int k = (int)min((int64_t)4, a.n - col);
-                if (parts)
-                    put4(parts + ((int64_t)split * a.rows + r) * a.n + col, v, k, false);
-                else
-                    put4((O*)a.y + r * a.ldy + col, v, k, a.accumulate != 0);
+            for (int i = 0; i < 4; ++i) {
+                const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[n][m][i]), __float_as_uint(acc[n + 1][m][i]),
+                                                                false, false);
+                const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+                v[i] = __uint_as_float(y[0]);
+                v[4 + i] = __uint_as_float(y[1]);
             }
+            const int64_t col = n0 + wn + 16 * n + 8 * (lane >> 4);
+            if (r >= a.rows || col >= a.n) continue;
+            const int k = (int)min((int64_t)8, a.n - col);
+            if (parts)
+                store8_n(parts + ((int64_t)split * a.rows + r) * a.n + col, Vec8<float>::put(v), k);
+            else
+                put8((O*)a.y + r * a.ldy, col, a.n, v, k, a.accumulate != 0);
+        }
     }
 }
 
@@ -453,9 +499,9 @@ hipError_t launch_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, const L
             else
                 by_type(dtype, [&](auto x) { e = launch_rows<decltype(x), O>(a, stream); });
         } else if (p.way == Way::TILE128) {
-            e = launch_tiles<EXACT, 2, O>(a, p.tile, (float*)ws, stream);
+            e = launch_tiles<EXACT, 4, O>(a, p.tile, (float*)ws, stream);
         } else if constexpr (!EXACT) {
-            e = launch_tiles<false, 4, O>(a, p.tile, (float*)ws, stream);
+            e = launch_tiles<false, 8, O>(a, p.tile, (float*)ws, stream);
         }
     });
     return e;
