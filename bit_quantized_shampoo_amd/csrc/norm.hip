@@ -37,28 +37,41 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t m) {
     return max(w[0], w[1]);
 }
 
-// Sums and maxima over the WPR waves of a row.  Consecutive reductions of a kernel take other
-// slots: a slot is written again only after a barrier that follows its last read.
+// Sums and maxima over the WPR waves of a row.  A reduction's slot is written again only after a
+// barrier that follows its last read: the reductions of a row have slots of their own, and rows
+// take turns with two sets of them.
 template <int WPR>
 struct Row {
     float (*red)[WPR];
     int wave;
-    __device__ __forceinline__ float sum(float v, int slot) const {
+    // A sum in three steps, so that several share a barrier.
+    __device__ __forceinline__ float partial(float v, int slot) const {
         v = wave_sum(v);
+        if constexpr (WPR > 1) red[slot][wave] = v;
+        return v;
+    }
+    __device__ __forceinline__ void meet() const {
+        // of LDS alone: a row's loads that are on their way, and stores, are not waited for
+        if constexpr (WPR > 1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+    __device__ __forceinline__ float total(float v, int slot) const {
         if constexpr (WPR > 1) {
-            red[slot][wave] = v;
-            __syncthreads();
             v = red[slot][0];
 #pragma unroll
             for (int i = 1; i < WPR; ++i) v += red[slot][i];
         }
         return v;
     }
+    __device__ __forceinline__ float sum(float v, int slot) const {
+        v = partial(v, slot);
+        meet();
+        return total(v, slot);
+    }
     __device__ __forceinline__ uint32_t largest(uint32_t m, int slot) const {
         m = wave_max(m);
         if constexpr (WPR > 1) {
             red[slot][wave] = __uint_as_float(m);
-            __syncthreads();
+            meet();
             m = 0;
 #pragma unroll
             for (int i = 0; i < WPR; ++i) m = max(m, __float_as_uint(red[slot][i]));
@@ -67,29 +80,41 @@ struct Row {
     }
 };
 
-// A thread's columns: vectors of eight, 8 THREADS apart.
+// A thread's columns: vectors of eight, 8 THREADS apart.  Rows are addressed by the wave (their
+// pointers are in scalar registers), columns by 32-bit offsets.
 template <int THREADS, int VPT>
 struct Cols {
     int cols, t;
     bool whole;               // rows of whole vectors
+    __device__ __forceinline__ Cols(int cols_, int t_) : cols(cols_), t(t_), whole((cols_ & 7) == 0) {}
     __device__ __forceinline__ int at(int i) const { return (t + i * THREADS) * 8; }
     __device__ __forceinline__ int n(int i) const { return max(0, min(8, cols - at(i))); }
 
+    // No load is under a lane's own condition: a vector past the row's end is loaded eight from it, and
+    // shifted or masked.
     template <class T>
-    __device__ __forceinline__ void load(typename Vec8<T>::Raw (&r)[VPT], const T* row) const {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (whole) {
-                r[i] = load8(row + min(at(i), cols - 8));
-                r[i] &= at(i) < cols ? 0xffffffffu : 0u;
-            } else {
-                r[i] = load8_edge(row, at(i), cols);
-            }
-        }
+    __device__ __forceinline__ typename Vec8<T>::Raw vector(const T* row, int i) const {
+        if (cols < 8) return load8_edge(row, at(i), cols);
+        const int c0 = min(at(i), cols - 8);
+        typename Vec8<T>::Raw r = load8((const T*)((const char*)row + (uint32_t)c0 * (uint32_t)sizeof(T)));
+        if (whole)
+            r &= at(i) < cols ? 0xffffffffu : 0u;
+        else
+            r = shift_down<T>(r, min(8, at(i) - c0));
+        return r;
+    }
+    template <class T>
+    __device__ __forceinline__ void store_raw(T* row, int i, typename Vec8<T>::Raw v) const {
+        if (at(i) >= cols) return;
+        T* p = (T*)((char*)row + (uint32_t)at(i) * (uint32_t)sizeof(T));
+        if (whole)
+            store8(p, v);
+        else
+            store8_n(p, v, n(i));
     }
     template <class T>
     __device__ __forceinline__ void store(T* row, int i, floatx8 v) const {
-        if (n(i)) store8_n(row + at(i), Vec8<T>::put(v), n(i));
+        store_raw(row, i, Vec8<T>::put(v));
     }
     // eight values of a vector that every row shares; `none` where there is no vector
     __device__ __forceinline__ floatx8 shared(const float* p, int i, float none) const {
@@ -99,7 +124,7 @@ struct Cols {
             for (int j = 0; j < 8; ++j) f[j] = none;
             return f;
         }
-        return Vec8<float>::get(load8_edge(p, at(i), cols));
+        return Vec8<float>::get(vector(p, i));
     }
 };
 
@@ -108,13 +133,13 @@ struct Cols {
 // squares lose below 2^-149 is nothing beside eps >= 1e-30.)
 template <class T, int WPR, int VPT>
 __device__ __forceinline__ float reciprocal_norm(const typename Vec8<T>::Raw (&r)[VPT], float ss, int cols, float eps,
-                                                 const Row<WPR>& row) {
+                                                 const Row<WPR>& row, int slot) {
     float scale = 1.f;
     if (!(ss < 0x1p126f)) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) m = max(m, magnitude(Vec8<T>::get(r[i])));
-        m = row.largest(m, 2);
+        m = row.largest(m, slot);
         if (m < 0x7f800000u) {
             scale = __uint_as_float((254u - min(m >> 23, 253u)) << 23);
             float s = 0.f;
@@ -124,30 +149,61 @@ __device__ __forceinline__ float reciprocal_norm(const typename Vec8<T>::Raw (&r
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s = fmaf(f[j], f[j], s);
             }
-            ss = row.sum(s, 3);
+            ss = row.sum(s, slot + 1);
         }
     }
     return scale / sqrtf(ss / (float)cols + eps * scale * scale);
 }
 
+__device__ __forceinline__ int wave_index() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
 constexpr int rows_of(int wpr) { return wpr == 1 ? 4 : 1; }              // of a workgroup
 constexpr int threads_of(int wpr) { return 64 * wpr * rows_of(wpr); }
 
-template <class T, int WPR, int VPT>
+// The rows of a workgroup of the backward kernel (of each of its four waves, where a row is a wave's) are
+// first, first + stride, and so on.
+struct Rows {
+    int64_t first, stride;
+};
+template <int WPR>
+__device__ __forceinline__ Rows rows_here() {
+    return {(int64_t)blockIdx.x * rows_of(WPR) + (WPR == 1 ? wave_index() : 0), (int64_t)gridDim.x * rows_of(WPR)};
+}
+// A row's number that the compiler makes addresses of where they are used, in scalar registers, rather
+// than keep one for each stream and lane.
+__device__ __forceinline__ int64_t here(int64_t row) {
+    asm volatile("" : "+s"(row));
+    return row;
+}
+
+template <class T, int WPR, int VPT, bool DROP, bool TOKEN>
 __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockForward a, Drop d) {
     constexpr int THREADS = 64 * WPR;
-    __shared__ float red[4][WPR];
-    const int64_t row = (int64_t)blockIdx.x * rows_of(WPR) + (WPR == 1 ? threadIdx.x >> 6 : 0);
+    __shared__ float red[6][WPR];
+    const int64_t row = (int64_t)blockIdx.x * rows_of(WPR) + (WPR == 1 ? wave_index() : 0);
     if (row >= a.rows) return;                               // a wave that has its row alone
     const int t = threadIdx.x % THREADS, cols = (int)a.cols;
     const Row<WPR> sums{red, t >> 6};
-    const Cols<THREADS, VPT> c{cols, t, (cols & 7) == 0};
+    const Cols<THREADS, VPT> c(cols, t);
     using Raw = typename Vec8<T>::Raw;
-    Raw x[VPT], h[VPT], g[VPT];
-    c.template load<T>(x, (const T*)a.x + row * a.ldx);
+    Raw x[VPT], h[VPT] = {}, g[VPT] = {};
+    floatx8 w[VPT], p[VPT], gv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        x[i] = c.vector((const T*)a.x + row * a.ldx, i);
+        if (a.h) {
+            h[i] = c.vector((const T*)a.h + row * a.ldh, i);
+            if (TOKEN) g[i] = c.vector((const T*)a.gate + row * a.ldgate, i);
+        }
+    }
+    // on their way with the row: behind its sums they would be waited for
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        p[i] = c.shared(a.post, i, 1.f);
+        if (!TOKEN) gv[i] = c.shared((const float*)a.gate, i, 1.f);
+        w[i] = c.shared(a.weight, i, 0.f);
+    }
     if (a.h) {
-        c.template load<T>(h, (const T*)a.h + row * a.ldh);
-        if (a.gate_rows) c.template load<T>(g, (const T*)a.gate + row * a.ldgate);
         float hr = 1.f;
         if (a.post) {
             float ss = 0.f;
@@ -157,22 +213,20 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
             }
-            hr = reciprocal_norm<T, WPR, VPT>(h, sums.sum(ss, 0), cols, a.eps, sums);
+            hr = reciprocal_norm<T, WPR, VPT>(h, sums.sum(ss, 0), cols, a.eps, sums, 2);
             if (a.h_rstd && t == 0) stg(a.h_rstd + row, hr);
         }
         const uint64_t call = drop_call(d);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            floatx8 z = Vec8<T>::get(h[i]);
-            if (a.post) z = z * hr * c.shared(a.post, i, 1.f);
-            if (d.threshold) z = drop8(z, drop_keep8(d, call, row, c.at(i) >> 3), d.scale);
-            if (a.gate_rows)
+            floatx8 z = Vec8<T>::get(h[i]) * hr * p[i];
+            if (DROP) z = drop8(z, drop_keep8(d, call, row, c.at(i) >> 3), d.scale);
+            if (TOKEN)
                 z *= Vec8<T>::get(g[i]);
-            else if (a.gate)
-                z *= c.shared((const float*)a.gate, i, 1.f);
-            const floatx8 v = Vec8<T>::get(x[i]) * a.rho + z;
-            x[i] = Vec8<T>::put(v);
-            if (c.n(i)) store8_n((T*)a.out + row * a.ldout + c.at(i), x[i], c.n(i));
+            else
+                z *= gv[i];
+            x[i] = Vec8<T>::put(Vec8<T>::get(x[i]) * a.rho + z);
+            c.template store_raw<T>((T*)a.out + row * a.ldout, i, x[i]);
         }
     }
     if (!a.weight) return;
@@ -183,13 +237,13 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss = fmaf(f[j], f[j], ss);
     }
-    const float r = reciprocal_norm<T, WPR, VPT>(x, sums.sum(ss, 1), cols, a.eps, sums);
-    if (a.rstd && t == 0) stg(a.rstd + row, r);
+    const float rx = reciprocal_norm<T, WPR, VPT>(x, sums.sum(ss, 1), cols, a.eps, sums, 4);
+    if (a.rstd && t == 0) stg(a.rstd + row, rx);
     const int64_t pitch = fp8_pitch(cols), sp = fp8_scale_pitch(cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const Raw y = Vec8<T>::put(Vec8<T>::get(x[i]) * r * c.shared(a.weight, i, 0.f));
-        if (a.y && c.n(i)) store8_n((T*)a.y + row * a.ldy + c.at(i), y, c.n(i));
+        const Raw y = Vec8<T>::put(Vec8<T>::get(x[i]) * rx * w[i]);
+        if (a.y) c.template store_raw<T>((T*)a.y + row * a.ldy, i, y);
         if (a.yc) {
             const floatx8 f = Vec8<T>::get(y);
             const uint32_t e = fp8_exponent(max16(magnitude(f)));
@@ -199,95 +253,174 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
     }
 }
 
-// Workgroups of the backward kernel: two a CU, each with a fixed set of rows whose sums it keeps.
-constexpr int64_t BACK_GROUPS = 512;
-int64_t back_groups(int64_t rows, int wpr) {
-    return std::min<int64_t>((rows + rows_of(wpr) - 1) / rows_of(wpr), BACK_GROUPS);
-}
-
-template <class T, int WPR, int VPT>
+// With sixteen waves (128 registers a lane) a row does not stay in registers beside its sums: it is read
+// again, from L2.
+template <class T, int WPR, int VPT, bool DROP, bool TOKEN>
 __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBackward a, Drop d) {
     constexpr int THREADS = 64 * WPR, PER = rows_of(WPR);
-    __shared__ float red[2][WPR];
+    constexpr bool AGAIN = WPR > 8, AHEAD = VPT == 1;
+    __shared__ float red[6][WPR];
     const int t = threadIdx.x % THREADS, cols = (int)a.cols;
     const Row<WPR> sums{red, t >> 6};
-    const Cols<THREADS, VPT> c{cols, t, (cols & 7) == 0};
+    const Cols<THREADS, VPT> c(cols, t);
     using Raw = typename Vec8<T>::Raw;
+    const Rows rows = rows_here<WPR>();
     const float inv = 1.f / (float)cols;
     const uint64_t call = drop_call(d);
-    floatx8 w[VPT], p[VPT], gv[VPT], dw[VPT] = {}, dp[VPT] = {}, dg[VPT] = {};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        w[i] = c.shared(a.weight, i, 0.f);
-        p[i] = c.shared(a.post, i, 1.f);
-        gv[i] = c.shared(a.gate_rows ? nullptr : (const float*)a.gate, i, 1.f);
-    }
-    for (int64_t row = (int64_t)blockIdx.x * PER + (WPR == 1 ? threadIdx.x >> 6 : 0); row < a.rows;
-         row += (int64_t)gridDim.x * PER) {
-        Raw dy[VPT] = {}, dr[VPT] = {}, x[VPT] = {}, h[VPT] = {}, g[VPT] = {};
-        float rx = 0.f, hr = 1.f;
+    struct In {
+        Raw dy, dr, x, h, g;
+    };
+    const auto load = [&](int64_t row, int i) {
+        In in = {};
         if (a.weight) {
-            c.template load<T>(dy, (const T*)a.dy + row * a.lddy);
-            c.template load<T>(x, (const T*)a.x + row * a.ldx);
-            rx = ldg(a.rstd + row);
+            in.dy = c.vector((const T*)a.dy + row * a.lddy, i);
+            in.x = c.vector((const T*)a.x + row * a.ldx, i);
         }
-        if (a.dres) c.template load<T>(dr, (const T*)a.dres + row * a.lddres);
+        if (a.dres) in.dr = c.vector((const T*)a.dres + row * a.lddres, i);
         if (a.h) {
-            c.template load<T>(h, (const T*)a.h + row * a.ldh);
-            if (a.post) hr = ldg(a.h_rstd + row);
-            if (a.gate_rows) c.template load<T>(g, (const T*)a.gate + row * a.ldgate);
+            in.h = c.vector((const T*)a.h + row * a.ldh, i);
+            if (TOKEN) in.g = c.vector((const T*)a.gate + row * a.ldgate, i);
         }
-        float s = 0.f;
+        return in;
+    };
+    struct Factors {
+        float x, h;
+    };
+    const auto factors = [&](int64_t row) {
+        return Factors{a.weight ? ldg(a.rstd + row) : 0.f, a.h && a.post ? ldg(a.h_rstd + row) : 1.f};
+    };
+    struct Shared {
+        floatx8 w, p, g;
+    };
+    const auto shared = [&](int i) {
+        return Shared{c.shared(a.weight, i, 0.f), c.shared(a.post, i, 1.f), c.shared(TOKEN ? nullptr : (const float*)a.gate, i, 1.f)};
+    };
+    In now[AGAIN ? 1 : VPT], next[AHEAD ? VPT : 1];
+    Factors f_now = {}, f_next = {};
+    Shared vec[AGAIN ? 1 : VPT];
+    if (AHEAD && rows.first < a.rows) {
+        f_next = factors(rows.first);
+        next[0] = load(rows.first, 0);
+    }
+    if (!AGAIN)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) vec[i] = shared(i);
+    floatx8 dw[VPT] = {}, dp[VPT] = {}, dg[VPT] = {};
+    int set = 0;
+    for (int64_t r = rows.first; r < a.rows; r += rows.stride, set ^= 3) {
+        const int64_t row = here(r);
+        if constexpr (AHEAD) {
+            now[0] = next[0];
+            f_now = f_next;
+            if (row + rows.stride < a.rows) {                // the next row is on its way while this one is worked on
+                f_next = factors(row + rows.stride);
+                next[0] = load(row + rows.stride, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        } else {
+            f_now = factors(row);
+            if (!AGAIN)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) now[i] = load(row, i);
+        }
+        const float rx = f_now.x, hr = f_now.h;
+        // One reduction for both norms: mean(u hh) = sum q (dres + rstd (t - xh s)) is linear in s = mean(t xh), with
+        // q = drop(gate post) hh the same for every term.
+        float s = 0.f, qa = 0.f, qb = 0.f;
+        uint32_t keep[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const floatx8 xh = Vec8<T>::get(x[i]) * rx, y = Vec8<T>::get(dy[i]);
-            const floatx8 ty = y * w[i];
-            dw[i] += y * xh;
+            if (AGAIN) {
+                now[0] = load(row, i);
+                vec[0] = shared(i);
+            }
+            In& in = now[AGAIN ? 0 : i];
+            const Shared& v = vec[AGAIN ? 0 : i];
+            const floatx8 xh = Vec8<T>::get(in.x) * rx, ty = Vec8<T>::get(in.dy) * v.w;
 #pragma unroll
             for (int j = 0; j < 8; ++j) s = fmaf(ty[j], xh[j], s);
-        }
-        s = sums.sum(s, 0) * inv;
-        floatx8 u[VPT];
-        float s2 = 0.f;
+            if (DROP) keep[i] = drop_keep8(d, call, row, c.at(i) >> 3);
+            if (a.post) {
+                floatx8 q = Vec8<T>::get(in.h) * hr * v.p;
+                if (TOKEN)
+                    q *= Vec8<T>::get(in.g);
+                else
+                    q *= v.g;
+                if (DROP) q = drop8(q, keep[i], d.scale);
+                const floatx8 dr = Vec8<T>::get(in.dr);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const floatx8 xh = Vec8<T>::get(x[i]) * rx, ty = Vec8<T>::get(dy[i]) * w[i];
-            const floatx8 gx = Vec8<T>::get(dr[i]) + (ty - xh * s) * rx;
-            if (a.dx) c.template store<T>((T*)a.dx + row * a.lddx, i, gx * a.rho);
-            if (!a.h) continue;
-            const floatx8 hh = Vec8<T>::get(h[i]) * hr;
-            const uint32_t keep = d.threshold ? drop_keep8(d, call, row, c.at(i) >> 3) : 0xffu;
-            const floatx8 z = gx * drop8(hh * p[i], keep, d.scale);
-            if (a.gate_rows) {
-                if (a.dgate) c.template store<T>((T*)a.dgate + row * a.lddgate, i, z);
-            } else {
-                dg[i] += z;
+                for (int j = 0; j < 8; ++j) {
+                    qa = fmaf(q[j], fmaf(ty[j], rx, dr[j]), qa);
+                    qb = fmaf(q[j], xh[j], qb);
+                }
             }
-            const floatx8 dn = drop8(gx * (a.gate_rows ? Vec8<T>::get(g[i]) : gv[i]), keep, d.scale);
-            dp[i] += dn * hh;
-            u[i] = dn * p[i];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s2 = fmaf(u[i][j], hh[j], s2);
+            unpack_again(in.x);
+            unpack_again(in.dy);
+            unpack_again(in.dr);
+            unpack_again(in.h);
+            unpack_again(in.g);
+            if (VPT > 1) __builtin_amdgcn_sched_barrier(0);
         }
-        s2 = sums.sum(s2, 1) * inv;
-        if (!a.h || !a.dh) continue;
+        s = sums.partial(s, set);
+        if (a.post) {
+            qa = sums.partial(qa, set + 1);
+            qb = sums.partial(qb, set + 2);
+        }
+        sums.meet();
+        s = sums.total(s, set) * inv * rx;                   // rstd mean(t xh)
+        const float s2 = a.post ? (sums.total(qa, set + 1) - s * sums.total(qb, set + 2)) * inv * hr : 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (a.post) u[i] = (u[i] - Vec8<T>::get(h[i]) * hr * s2) * hr;
-            c.template store<T>((T*)a.dh + row * a.lddh, i, u[i]);
+            if (AGAIN) {
+                now[0] = load(row, i);
+                vec[0] = shared(i);
+            }
+            const In& in = now[AGAIN ? 0 : i];
+            const Shared& v = vec[AGAIN ? 0 : i];
+            const floatx8 xh = Vec8<T>::get(in.x) * rx, y = Vec8<T>::get(in.dy);
+            floatx8 gx = Vec8<T>::get(in.dr);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                dw[i][j] = fmaf(y[j], xh[j], dw[i][j]);
+                gx[j] = fmaf(xh[j], -s, fmaf(y[j] * v.w[j], rx, gx[j]));
+            }
+            if (a.dx) c.template store<T>((T*)a.dx + row * a.lddx, i, gx * a.rho);
+            if (a.h) {
+                const floatx8 hh = Vec8<T>::get(in.h) * hr;
+                floatx8 z = hh * v.p;                        // what the gate multiplies
+                if (DROP) {
+                    gx = drop8(gx, keep[i], d.scale);        // dropped: no gradient, and z counts for nothing
+                    z = drop8(z, keep[i], 1.f);
+                }
+                if (TOKEN) {
+                    if (a.dgate) c.template store<T>((T*)a.dgate + row * a.lddgate, i, gx * z);
+                    gx *= Vec8<T>::get(in.g);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) dg[i][j] = fmaf(gx[j], z[j], dg[i][j]);
+                    gx *= v.g;
+                }
+                if (a.post) {
+                    // dh = rstd (u - hh mean(u hh))
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        dp[i][j] = fmaf(gx[j], hh[j], dp[i][j]);
+                        gx[j] = fmaf(gx[j] * v.p[j], hr, -hh[j] * s2);
+                    }
+                }
+                if (a.dh) c.template store<T>((T*)a.dh + row * a.lddh, i, gx);
+            }
+            if (VPT > 1) __builtin_amdgcn_sched_barrier(0);  // one vector's values at a time in registers
         }
     }
     if (!a.parts) return;
     float* out = a.parts + (int64_t)blockIdx.x * 3 * cols;
-    const auto write = [&](float* to, floatx8 v, int i) {
-        if (c.n(i)) store8_n(to + c.at(i), Vec8<float>::put(v), c.n(i));
-    };
     if constexpr (PER == 1) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            write(out, dw[i], i);
-            write(out + cols, dp[i], i);
-            write(out + 2 * cols, dg[i], i);
+            c.template store<float>(out, i, dw[i]);
+            c.template store<float>(out + cols, i, dp[i]);
+            c.template store<float>(out + 2 * cols, i, dg[i]);
         }
     } else {
         // the waves' sums, wave by wave
@@ -327,24 +460,46 @@ __global__ __launch_bounds__(256) void block_join_kernel(const float* parts, Joi
     if (q == 0 && col < cols) stg(out + col, ((run[0][l] + run[1][l]) + run[2][l]) + run[3][l]);
 }
 
-// Waves and vectors a row takes: up to two vectors a lane (their registers, with the sums over rows, are
-// what two waves a SIMD leave), then more waves.
-int waves_of(int64_t cols) { return cols <= 1024 ? 1 : cols <= 4096 ? 4 : cols <= 8192 ? 8 : 16; }
-
-template <class F>
+// Calls f(waves a row takes, vectors a lane takes).
+template <bool FORWARD, class F>
 void by_row(int64_t cols, F f) {
-    const auto vectors = [&](auto w) {
-        if (cols <= 512 * decltype(w)::value)
-            f(w, std::integral_constant<int, 1>{});
-        else
-            f(w, std::integral_constant<int, 2>{});
-    };
-    switch (waves_of(cols)) {
-        case 1: return vectors(std::integral_constant<int, 1>{});
-        case 4: return vectors(std::integral_constant<int, 4>{});
-        case 8: return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
-        default: return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, 4> four{};
+    constexpr std::integral_constant<int, 8> eight{};
+    constexpr std::integral_constant<int, 16> sixteen{};
+    if (cols <= 512) return f(one, one);
+    if (cols <= 1024) return f(two, one);
+    if (cols <= 2048) return f(four, one);
+    if (cols <= 4096) return f(eight, one);
+    if constexpr (FORWARD) {
+        if (cols <= 8192) return f(sixteen, one);
+        f(sixteen, two);
+    } else {
+        if (cols <= 8192) return f(eight, two);
+        f(sixteen, two);
     }
+}
+// Calls f(dropout, gate by element).
+template <class F>
+void by_form(bool drop, bool token, F f) {
+    if (drop)
+        token ? f(std::true_type{}, std::true_type{}) : f(std::true_type{}, std::false_type{});
+    else
+        token ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{});
+}
+
+int64_t workgroups(int64_t rows, int wpr, int64_t most) {
+    return std::min<int64_t>((rows + rows_of(wpr) - 1) / rows_of(wpr), most);
+}
+// Of the backward kernel: eight waves a CU, each with a fixed set of rows whose sums it keeps.
+int64_t back_groups(int64_t rows, int64_t cols) {
+    int64_t n = 0;
+    by_row<false>(cols, [&](auto w, auto) {
+        constexpr int W = decltype(w)::value;
+        n = workgroups(rows, W, 256 * std::max(1, 8 / (W * rows_of(W))));
+    });
+    return n;
 }
 
 }  // namespace
@@ -353,17 +508,19 @@ hipError_t launch_block_forward(shampoo4_dtype dtype, const BlockForward& a, con
     if (a.rows <= 0) return hipSuccess;
     by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        by_row(a.cols, [&](auto w, auto v) {
+        by_row<true>(a.cols, [&](auto w, auto v) {
             constexpr int W = decltype(w)::value, V = decltype(v)::value;
-            S4_LAUNCH((block_forward_kernel<T, W, V>), dim3((uint32_t)((a.rows + rows_of(W) - 1) / rows_of(W))),
-                      dim3(threads_of(W)), 0, stream, a, d);
+            by_form(d.threshold && a.h, a.gate_rows, [&](auto drop, auto token) {
+                S4_LAUNCH((block_forward_kernel<T, W, V, decltype(drop)::value, decltype(token)::value>),
+                          dim3((uint32_t)((a.rows + rows_of(W) - 1) / rows_of(W))), dim3(threads_of(W)), 0, stream, a, d);
+            });
         });
     });
     return hipGetLastError();
 }
 
 size_t block_workspace_bytes(int64_t rows, int64_t cols) {
-    return (size_t)back_groups(rows, waves_of(cols)) * 3 * cols * 4;
+    return (size_t)back_groups(rows, cols) * 3 * cols * 4;
 }
 
 hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& given, const Drop& d, hipStream_t stream) {
@@ -371,13 +528,16 @@ hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& give
     const Join j{{a.dweight, a.dpost, a.gate_rows ? nullptr : (float*)a.dgate}};
     const bool join = j.out[0] || j.out[1] || j.out[2];
     if (!join) a.parts = nullptr;
-    const int64_t groups = back_groups(a.rows, waves_of(a.cols));
+    const int64_t groups = back_groups(a.rows, a.cols);
     if (groups > 0)
         by_type(dtype, [&](auto t) {
             using T = decltype(t);
-            by_row(a.cols, [&](auto w, auto v) {
+            by_row<false>(a.cols, [&](auto w, auto v) {
                 constexpr int W = decltype(w)::value, V = decltype(v)::value;
-                S4_LAUNCH((block_backward_kernel<T, W, V>), dim3((uint32_t)groups), dim3(threads_of(W)), 0, stream, a, d);
+                by_form(d.threshold && a.h, a.gate_rows, [&](auto drop, auto token) {
+                    S4_LAUNCH((block_backward_kernel<T, W, V, decltype(drop)::value, decltype(token)::value>),
+                              dim3((uint32_t)groups), dim3(threads_of(W)), 0, stream, a, d);
+                });
             });
         });
     if (join)
