@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, i
     for (int i = 0; i < ROWS; ++i) {
         if (row0 + i >= rows || n == 0) continue;
         if (d.threshold)
-            r[i] = Vec8<T>::put(drop8(Vec8<T>::get(r[i]), drop_keep8(d, call, row0 + i, col >> 3), d.scale));
+            r[i] = Vec8<T>::put(drop8(Vec8<T>::get(r[i]) * d.scale, drop_keep8(d, call, row0 + i, col >> 3), d));
         store8_n(y + (row0 + i) * ldy + col, r[i], n);
     }
 }

@@ -90,18 +90,20 @@ struct Cols {
     __device__ __forceinline__ int at(int i) const { return (t + i * THREADS) * 8; }
     __device__ __forceinline__ int n(int i) const { return max(0, min(8, cols - at(i))); }
 
-    // No load is under a lane's own condition: a vector past the row's end is loaded eight from it, and
-    // shifted or masked.
+    // No load is under a lane's own condition: a vector past the row's end is loaded eight from it.  What was
+    // loaded is finished where it is used, so that loads are not waited for one by one: shifted, or
+    // masked.
     template <class T>
     __device__ __forceinline__ typename Vec8<T>::Raw vector(const T* row, int i) const {
         if (cols < 8) return load8_edge(row, at(i), cols);
-        const int c0 = min(at(i), cols - 8);
-        typename Vec8<T>::Raw r = load8((const T*)((const char*)row + (uint32_t)c0 * (uint32_t)sizeof(T)));
+        return load8((const T*)((const char*)row + (uint32_t)min(at(i), cols - 8) * (uint32_t)sizeof(T)));
+    }
+    template <class T>
+    __device__ __forceinline__ void finish(typename Vec8<T>::Raw& r, int i) const {
         if (whole)
             r &= at(i) < cols ? 0xffffffffu : 0u;
-        else
-            r = shift_down<T>(r, min(8, at(i) - c0));
-        return r;
+        else if (cols >= 8)
+            r = shift_down<T>(r, min(8, max(0, at(i) - (cols - 8))));
     }
     template <class T>
     __device__ __forceinline__ void store_raw(T* row, int i, typename Vec8<T>::Raw v) const {
@@ -116,15 +118,18 @@ struct Cols {
     __device__ __forceinline__ void store(T* row, int i, floatx8 v) const {
         store_raw(row, i, Vec8<T>::put(v));
     }
-    // eight values of a vector that every row shares; `none` where there is no vector
-    __device__ __forceinline__ floatx8 shared(const float* p, int i, float none) const {
-        floatx8 f;
-        if (!p) {
+    // Eight values of a vector that every row shares, and how they are finished; ones where there is no
+    // vector.
+    __device__ __forceinline__ u32x8 shared(const float* p, int i) const {
+        if (p) return vector(p, i);
+        u32x8 one;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = none;
-            return f;
-        }
-        return Vec8<float>::get(vector(p, i));
+        for (int j = 0; j < 8; ++j) one[j] = 0x3f800000u;
+        return one;
+    }
+    __device__ __forceinline__ floatx8 finish_shared(const float* p, u32x8 r, int i) const {
+        if (p) finish<float>(r, i);
+        return Vec8<float>::get(r);
     }
 };
 
@@ -187,7 +192,7 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
     const Cols<THREADS, VPT> c(cols, t);
     using Raw = typename Vec8<T>::Raw;
     Raw x[VPT], h[VPT] = {}, g[VPT] = {};
-    floatx8 w[VPT], p[VPT], gv[VPT];
+    u32x8 rw[VPT], rp[VPT], rg[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         x[i] = c.vector((const T*)a.x + row * a.ldx, i);
@@ -199,11 +204,25 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
     // on their way with the row: behind its sums they would be waited for
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        p[i] = c.shared(a.post, i, 1.f);
-        if (!TOKEN) gv[i] = c.shared((const float*)a.gate, i, 1.f);
-        w[i] = c.shared(a.weight, i, 0.f);
+        rp[i] = c.shared(a.post, i);
+        if (!TOKEN) rg[i] = c.shared((const float*)a.gate, i);
+        rw[i] = c.shared(a.weight, i);
     }
+    Keep keep[DROP ? VPT : 1];
+    if (DROP) {                                              // while all that is on its way
+        const uint64_t call = drop_call(d);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) keep[i] = drop_keep8(d, call, row, c.at(i) >> 3);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) c.template finish<T>(x[i], i);
     if (a.h) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            c.template finish<T>(h[i], i);
+            if (TOKEN) c.template finish<T>(g[i], i);
+        }
         float hr = 1.f;
         if (a.post) {
             float ss = 0.f;
@@ -216,15 +235,14 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
             hr = reciprocal_norm<T, WPR, VPT>(h, sums.sum(ss, 0), cols, a.eps, sums, 2);
             if (a.h_rstd && t == 0) stg(a.h_rstd + row, hr);
         }
-        const uint64_t call = drop_call(d);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            floatx8 z = Vec8<T>::get(h[i]) * hr * p[i];
-            if (DROP) z = drop8(z, drop_keep8(d, call, row, c.at(i) >> 3), d.scale);
+            floatx8 z = Vec8<T>::get(h[i]) * (DROP ? hr * d.scale : hr) * c.finish_shared(a.post, rp[i], i);
+            if (DROP) z = drop8(z, keep[i], d);
             if (TOKEN)
                 z *= Vec8<T>::get(g[i]);
             else
-                z *= gv[i];
+                z *= c.finish_shared((const float*)a.gate, rg[i], i);
             x[i] = Vec8<T>::put(Vec8<T>::get(x[i]) * a.rho + z);
             c.template store_raw<T>((T*)a.out + row * a.ldout, i, x[i]);
         }
@@ -242,7 +260,7 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
     const int64_t pitch = fp8_pitch(cols), sp = fp8_scale_pitch(cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const Raw y = Vec8<T>::put(Vec8<T>::get(x[i]) * rx * w[i]);
+        const Raw y = Vec8<T>::put(Vec8<T>::get(x[i]) * rx * c.finish_shared(a.weight, rw[i], i));
         if (a.y) c.template store_raw<T>((T*)a.y + row * a.ldy, i, y);
         if (a.yc) {
             const floatx8 f = Vec8<T>::get(y);
@@ -256,7 +274,7 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
 // With sixteen waves (128 registers a lane) a row does not stay in registers beside its sums: it is read
 // again, from L2.
 template <class T, int WPR, int VPT, bool DROP, bool TOKEN>
-__global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBackward a, Drop d) {
+__global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(BlockBackward a, Drop d) {
     constexpr int THREADS = 64 * WPR, PER = rows_of(WPR);
     constexpr bool AGAIN = WPR > 8, AHEAD = VPT == 1;
     __shared__ float red[6][WPR];
@@ -283,6 +301,13 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
         }
         return in;
     };
+    const auto finish = [&](In& in, int i) {
+        c.template finish<T>(in.dy, i);
+        c.template finish<T>(in.x, i);
+        c.template finish<T>(in.dr, i);
+        c.template finish<T>(in.h, i);
+        if (TOKEN) c.template finish<T>(in.g, i);
+    };
     struct Factors {
         float x, h;
     };
@@ -292,8 +317,13 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
     struct Shared {
         floatx8 w, p, g;
     };
+    // What is kept of dropout is scaled by way of the gate (a gate by element is scaled itself) and of the sums.
+    const float drop_scale = DROP ? d.scale : 1.f;
+    const float* gate = TOKEN ? nullptr : (const float*)a.gate;
     const auto shared = [&](int i) {
-        return Shared{c.shared(a.weight, i, 0.f), c.shared(a.post, i, 1.f), c.shared(TOKEN ? nullptr : (const float*)a.gate, i, 1.f)};
+        const u32x8 w = c.shared(a.weight, i), p = c.shared(a.post, i), g = c.shared(gate, i);
+        return Shared{c.finish_shared(a.weight, w, i), c.finish_shared(a.post, p, i),
+                      c.finish_shared(gate, g, i) * (TOKEN ? 1.f : drop_scale)};
     };
     In now[AGAIN ? 1 : VPT], next[AHEAD ? VPT : 1];
     Factors f_now = {}, f_next = {};
@@ -309,8 +339,17 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
     int set = 0;
     for (int64_t r = rows.first; r < a.rows; r += rows.stride, set ^= 3) {
         const int64_t row = here(r);
+        Keep keep[DROP ? VPT : 1];
+        const auto numbers = [&]() {                         // while the row is on its way
+            if (DROP)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) keep[i] = drop_keep8(d, call, row, c.at(i) >> 3);
+            __builtin_amdgcn_sched_barrier(0);
+        };
         if constexpr (AHEAD) {
+            numbers();
             now[0] = next[0];
+            finish(now[0], 0);
             f_now = f_next;
             if (row + rows.stride < a.rows) {                // the next row is on its way while this one is worked on
                 f_next = factors(row + rows.stride);
@@ -322,31 +361,34 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
             if (!AGAIN)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) now[i] = load(row, i);
+            numbers();
+            if (!AGAIN)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) finish(now[i], i);
         }
         const float rx = f_now.x, hr = f_now.h;
         // One reduction for both norms: mean(u hh) = sum q (dres + rstd (t - xh s)) is linear in s = mean(t xh), with
         // q = drop(gate post) hh the same for every term.
         float s = 0.f, qa = 0.f, qb = 0.f;
-        uint32_t keep[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (AGAIN) {
                 now[0] = load(row, i);
                 vec[0] = shared(i);
+                finish(now[0], i);
             }
             In& in = now[AGAIN ? 0 : i];
             const Shared& v = vec[AGAIN ? 0 : i];
             const floatx8 xh = Vec8<T>::get(in.x) * rx, ty = Vec8<T>::get(in.dy) * v.w;
 #pragma unroll
             for (int j = 0; j < 8; ++j) s = fmaf(ty[j], xh[j], s);
-            if (DROP) keep[i] = drop_keep8(d, call, row, c.at(i) >> 3);
             if (a.post) {
                 floatx8 q = Vec8<T>::get(in.h) * hr * v.p;
                 if (TOKEN)
                     q *= Vec8<T>::get(in.g);
                 else
                     q *= v.g;
-                if (DROP) q = drop8(q, keep[i], d.scale);
+                if (DROP) q = drop8(q, keep[i], d);
                 const floatx8 dr = Vec8<T>::get(in.dr);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -368,12 +410,13 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
         }
         sums.meet();
         s = sums.total(s, set) * inv * rx;                   // rstd mean(t xh)
-        const float s2 = a.post ? (sums.total(qa, set + 1) - s * sums.total(qb, set + 2)) * inv * hr : 0.f;
+        const float s2 = a.post ? (sums.total(qa, set + 1) - s * sums.total(qb, set + 2)) * inv * (TOKEN ? hr * drop_scale : hr) : 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (AGAIN) {
                 now[0] = load(row, i);
                 vec[0] = shared(i);
+                finish(now[0], i);
             }
             const In& in = now[AGAIN ? 0 : i];
             const Shared& v = vec[AGAIN ? 0 : i];
@@ -389,10 +432,11 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
                 const floatx8 hh = Vec8<T>::get(in.h) * hr;
                 floatx8 z = hh * v.p;                        // what the gate multiplies
                 if (DROP) {
-                    gx = drop8(gx, keep[i], d.scale);        // dropped: no gradient, and z counts for nothing
-                    z = drop8(z, keep[i], 1.f);
+                    gx = drop8(gx, keep[i], d);              // dropped: no gradient
+                    if (!a.post) z = drop8(z, keep[i], d);   // and h may be anything
                 }
                 if (TOKEN) {
+                    gx *= drop_scale;
                     if (a.dgate) c.template store<T>((T*)a.dgate + row * a.lddgate, i, gx * z);
                     gx *= Vec8<T>::get(in.g);
                 } else {
@@ -414,6 +458,9 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_backward_kernel(BlockBa
         }
     }
     if (!a.parts) return;
+    if (DROP)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) dg[i] *= drop_scale;
     float* out = a.parts + (int64_t)blockIdx.x * 3 * cols;
     if constexpr (PER == 1) {
 #pragma unroll
@@ -465,19 +512,24 @@ template <bool FORWARD, class F>
 void by_row(int64_t cols, F f) {
     constexpr std::integral_constant<int, 1> one{};
     constexpr std::integral_constant<int, 2> two{};
+    constexpr std::integral_constant<int, 3> three{};
     constexpr std::integral_constant<int, 4> four{};
     constexpr std::integral_constant<int, 8> eight{};
+    constexpr std::integral_constant<int, 12> twelve{};
     constexpr std::integral_constant<int, 16> sixteen{};
     if (cols <= 512) return f(one, one);
-    if (cols <= 1024) return f(two, one);
-    if (cols <= 2048) return f(four, one);
-    if (cols <= 4096) return f(eight, one);
     if constexpr (FORWARD) {
+        if (cols <= 1024) return f(two, one);
+        if (cols <= 2048) return f(four, one);
+        if (cols <= 4096) return f(eight, one);
         if (cols <= 8192) return f(sixteen, one);
         f(sixteen, two);
     } else {
+        if (cols <= 1024) return f(one, two);
+        if (cols <= 2048) return f(two, two);
+        if (cols <= 4096) return f(four, two);
         if (cols <= 8192) return f(eight, two);
-        f(sixteen, two);
+        f(twelve, three);
     }
 }
 // Calls f(dropout, gate by element).

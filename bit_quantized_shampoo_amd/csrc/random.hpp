@@ -35,21 +35,21 @@ __device__ __forceinline__ u32x4 philox(uint32_t x0, uint32_t x1, uint64_t call,
     return u32x4{x0, x1, x2, x3};
 }
 
-// Bit j: column 8 col8 + j of the row is kept.
-__device__ __forceinline__ uint32_t drop_keep8(const Drop& d, uint64_t call, int64_t row, int64_t col8) {
-    const u32x4 w = philox((uint32_t)col8, (uint32_t)row, call, d.seed);
-    uint32_t keep = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t r = j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xffffu;
-        keep |= (r >= d.threshold ? 1u : 0u) << j;
+// The numbers of eight columns, 8 col8 on, of a row, and which of them are kept: the comparison of a
+// half is one of whole words (the lower half brought up, the upper one with what is below it).
+struct Keep {
+    u32x4 w;
+    __device__ __forceinline__ bool operator()(int j, const Drop& d) const {
+        return (j & 1 ? w[j >> 1] : w[j >> 1] << 16) >= d.threshold << 16;
     }
-    return keep;
+};
+__device__ __forceinline__ Keep drop_keep8(const Drop& d, uint64_t call, int64_t row, int64_t col8) {
+    return {philox((uint32_t)col8, (uint32_t)row, call, d.seed)};
 }
-// Kept values scaled, others 0 whatever they were.
-__device__ __forceinline__ floatx8 drop8(floatx8 x, uint32_t keep, float scale) {
+// Zeros for what is dropped, whatever it was (the rest has still to be scaled).
+__device__ __forceinline__ floatx8 drop8(floatx8 x, const Keep& keep, const Drop& d) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = keep >> j & 1 ? x[j] * scale : 0.f;
+    for (int j = 0; j < 8; ++j) x[j] = keep(j, d) ? x[j] : 0.f;
     return x;
 }
 
