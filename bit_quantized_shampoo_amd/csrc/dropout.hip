@@ -21,10 +21,11 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, i
     const uint64_t call = drop_call(d);
     typename Vec8<T>::Raw r[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) r[i] = load8_edge(x + min(row0 + i, rows - 1) * ldx, col, cols);
+    for (int i = 0; i < ROWS; ++i) r[i] = load8_near(x + min(row0 + i, rows - 1) * ldx, col, cols);
     const int n = (int)max((int64_t)0, min((int64_t)8, cols - col));
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
+        finish8<T>(r[i], col, cols);
         if (row0 + i >= rows || n == 0) continue;
         if (d.threshold)
             r[i] = Vec8<T>::put(drop8(Vec8<T>::get(r[i]) * d.scale, drop_keep8(d, call, row0 + i, col >> 3), d));

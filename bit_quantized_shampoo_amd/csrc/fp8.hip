@@ -24,9 +24,10 @@ __global__ __launch_bounds__(256) void fp8_store_kernel(const T* __restrict__ x,
     const int64_t pitch = fp8_pitch(cols), sp = fp8_scale_pitch(cols);
     typename Vec8<T>::Raw r[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) r[i] = load8_edge(x + min(row0 + i, rows - 1) * ldx, col, cols);
+    for (int i = 0; i < ROWS; ++i) r[i] = load8_near(x + min(row0 + i, rows - 1) * ldx, col, cols);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
+        finish8<T>(r[i], col, cols);
         const floatx8 f = Vec8<T>::get(r[i]);
         const uint32_t e = fp8_exponent(max16(magnitude(f)));
         if (row0 + i >= rows) break;
@@ -50,10 +51,11 @@ __global__ __launch_bounds__(256) void fp8_weight_kernel(const T* __restrict__ w
     const int c = (tid & 15) * 8, r0 = tid >> 4;
     typename Vec8<T>::Raw r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = load8_edge(w + min(row0 + r0 + 16 * i, rows - 1) * ldw, col0 + c, cols);
+    for (int i = 0; i < 8; ++i) r[i] = load8_near(w + min(row0 + r0 + 16 * i, rows - 1) * ldw, col0 + c, cols);
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+        finish8<T>(r[i], col0 + c, cols);
         r[i] &= row0 + r0 + 16 * i < rows ? 0xffffffffu : 0u;
         m = max(m, magnitude(Vec8<T>::get(r[i])));
     }

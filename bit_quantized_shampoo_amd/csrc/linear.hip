@@ -69,10 +69,10 @@ __device__ __forceinline__ void put8(O* row, int64_t col, int64_t cols, floatx8 
 // X's element type as a kernel's parameter: uint8_t where it is given as codes.
 constexpr int WAVES = 8;
 
-template <class X, class O, int MT>
+// MT: sixteens of rows; AHEAD: blocks of k that a wave has in flight.
+template <class X, class O, int MT, int AHEAD>
 __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(Linear a, uint32_t tiles_n) {
-    constexpr bool EXACT = !std::is_same_v<O, __bf16>;
-    constexpr int AHEAD = 2;                                 // blocks of k in flight
+    constexpr bool EXACT = !std::is_same_v<O, __bf16>, CODES = std::is_same_v<X, uint8_t>;
     __shared__ floatx4 sums[WAVES][MT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t n0 = (int64_t)(blockIdx.x % tiles_n) * 16, m0 = (int64_t)(blockIdx.x / tiles_n) * (16 * MT);
@@ -85,6 +85,9 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(Linear a, uint3
     for (int kb0 = wave; kb0 < nkb; kb0 += AHEAD * WAVES) {
         Frag fw[AHEAD], fx[AHEAD][MT];
         uint32_t we[AHEAD], xe[AHEAD][MT];
+        using V = std::conditional_t<CODES, float, X>;
+        typename Vec8<V>::Raw raw[CODES ? 1 : AHEAD][CODES ? 1 : MT][4];
+        // every load first
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             const int64_t kb = min(kb0 + u * WAVES, nkb - 1);
@@ -94,31 +97,40 @@ __global__ __launch_bounds__(64 * WAVES) void linear_rows_kernel(Linear a, uint3
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 const int64_t row = min(m0 + 16 * t + r, a.rows - 1);
-                if constexpr (std::is_same_v<X, uint8_t>) {
+                if constexpr (CODES) {
                     const uint8_t* x = a.xc + row * pitch + kb * 128 + kq;
                     fx[u][t].lo = ldg((const u32x4*)x);
                     fx[u][t].hi = ldg((const u32x4*)(x + 16));
                     xe[u][t] = ldg(a.xs + row * sp + kb);
                 } else {
-                    const X* x = (const X*)a.x + row * a.ldx;
-                    floatx8 f[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) raw[u][t][q] = load8_near((const X*)a.x + row * a.ldx, kb * 128 + kq + 8 * q, a.k);
+                }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!CODES) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const int64_t c = min(kb0 + u * WAVES, nkb - 1) * 128ll + kq;
                     uint32_t m = 0;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        f[q] = Vec8<X>::get(load8_edge(x, kb * 128 + kq + 8 * q, a.k));
-                        m = max(m, magnitude(f[q]));
+                        finish8<X>(raw[u][t][q], c + 8 * q, a.k);
+                        m = max(m, magnitude(Vec8<X>::get(raw[u][t][q])));
                     }
                     xe[u][t] = fp8_exponent(max_of_rows(m));
                     const Fp8Block blk(xe[u][t]);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const u32x2 c = blk.codes(f[q]);
+                        const u32x2 c8 = blk.codes(Vec8<X>::get(raw[u][t][q]));
                         u32x4& to = q < 2 ? fx[u][t].lo : fx[u][t].hi;
-                        to[q % 2 * 2] = c[0];
-                        to[q % 2 * 2 + 1] = c[1];
+                        to[q % 2 * 2] = c8[0];
+                        to[q % 2 * 2 + 1] = c8[1];
                     }
                 }
-            }
         }
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
@@ -393,53 +405,88 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
     }
 }
 
-// Y (+)= the ranges' sums, in order.
-template <class O>
+// Y (+)= the ranges' sums, in order; V consecutive elements of a row a thread.
+template <class O, int V>
 __global__ __launch_bounds__(256) void linear_join_kernel(Linear a, const float* parts, int splits) {
+    typedef float Vec __attribute__((ext_vector_type(V)));
+    typedef Vec Mem __attribute__((aligned(4)));
+    using G = __attribute__((address_space(1))) const Mem;
     const int64_t count = a.rows * a.n;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) {
-        float s = ldg(parts + i);
-        for (int k = 1; k < splits; ++k) s += ldg(parts + k * count + i);
-        O* p = (O*)a.y + i / a.n * a.ldy + i % a.n;
-        stg(p, (O)(a.accumulate ? (float)ldg(p) + s : s));
+    for (int64_t i = (blockIdx.x * 256ll + threadIdx.x) * V; i < count; i += gridDim.x * 256ll * V) {
+        Vec s = *(G*)(parts + i);
+        for (int k = 1; k < splits; ++k) s += *(G*)(parts + k * count + i);
+        const int64_t row = i / a.n;
+        O* p = (O*)a.y + row * a.ldy + (i - row * a.n);
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = a.accumulate ? (float)ldg(p + j) + s[j] : s[j];
+#pragma unroll
+        for (int j = 0; j < V; ++j) stg(p + j, (O)f[j]);
     }
 }
 
 size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
-// How a product is done: by rows of X and 16 columns of Y a workgroup, or by tiles.
-enum class Way { ROWS, TILE128, TILE256 };
+// How a product is done: by rows of X and 16 columns of Y a workgroup, or by tiles of 32 T a side.
 struct LinearPlan {
-    Way way;
-    TilePlan tile;
+    int tile;                 // T; 0: by rows
+    TilePlan plan;
 };
+
+// Few rows read W as it lies, and quantise X within the product; beyond 16 rows that is worth it while the
+// workgroups that do it again are few and k is short (64 x 4096 x 1024 takes 6.0 us by rows and
+// 5.8 on tiles after 3.9 for quantising).
+//
+// Tiles and ranges of k by an estimate of the time, of what was measured: with c workgroups a CU, a block of
+// k takes 0.2 c us on 64 x 64 tiles (0.23 at least), 0.1 + 0.46 c on 128 x 128 and 1.3 c on 256 x 256;
+// with exact products 0.3 + 0.33 c and 1.26 c (1.45 at least).  Beside that a launch takes 4 us (8 on
+// the largest tiles), and joining ranges 3 us and their bytes.  1024 x 4096 x 4096 bf16 takes 29.7,
+// 23.4 and 47 us on the three tiles, 777 x 577 x 1153 7.3, 10.5 and 28, 4096 x 4096 x 1024 33, 27 and
+// 23.5, 8192 x 1024 x 4096 53, 33 and 50; 300 x 300 x 4096 fp32 22 us in one range and 12 in four.
 LinearPlan linear_plan(bool exact, int64_t rows, int64_t n, int64_t k) {
-    LinearPlan p{};
-    p.way = Way::ROWS;
+    LinearPlan best{};
     const int64_t pitch = fp8_pitch(k);
-    if (rows <= 64 || pitch > (1 << 23)) return p;
+    if (rows <= 16 || (rows <= 64 && n <= 8192 && k <= 2048) || pitch > (1 << 23)) return best;
     const int nkb = (int)(pitch >> 7);
-    const auto tiles = [&](int side) { return ((rows + side - 1) / side) * ((n + side - 1) / side); };
-    const int side = !exact && tiles(256) >= 192 ? 256 : 128;
-    p.way = side == 256 ? Way::TILE256 : Way::TILE128;
-    p.tile.tiles_m = (int)((rows + side - 1) / side);
-    p.tile.tiles_n = (int)((n + side - 1) / side);
-    int splits = 1;
-    while (side == 128 && splits < 16 && tiles(128) * splits * 2 <= 512 && nkb >= 8 * splits) splits *= 2;
-    p.tile.blocks = ((nkb + splits - 1) / splits + 3) / 4 * 4;
-    p.tile.splits = (nkb + p.tile.blocks - 1) / p.tile.blocks;
-    return p;
+    double best_us = 0;
+    for (int t = 2; t <= (exact ? 4 : 8); t *= 2) {
+        const int64_t side = 32 * t;
+        LinearPlan p{t, {(int)((rows + side - 1) / side), (int)((n + side - 1) / side), 1, 0}};
+        const int64_t tiles = (int64_t)p.plan.tiles_m * p.plan.tiles_n;
+        for (int s = 1; s <= 16 && (s == 1 || (nkb >= 8 * s && tiles * s <= 1024)); s *= 2) {
+            p.plan.blocks = ((nkb + s - 1) / s + 3) / 4 * 4;
+            p.plan.splits = (nkb + p.plan.blocks - 1) / p.plan.blocks;
+            const double c = (double)((tiles * p.plan.splits + 255) / 256);
+            const double block = exact ? (t == 2 ? 0.3 + 0.33 * c : std::max(1.45, 1.26 * c))
+                                       : (t == 2 ? std::max(0.23, 0.2 * c) : t == 4 ? 0.1 + 0.46 * c : 1.3 * c);
+            double us = block * std::min(p.plan.blocks, nkb) + (t == 8 ? 8. : 4.);
+            if (p.plan.splits > 1) us += 3. + (2. * p.plan.splits + 1) * (double)(rows * n) * 4 / 5e6;
+            if (best_us == 0 || us < best_us) {
+                best = p;
+                best_us = us;
+            }
+        }
+    }
+    return best;
 }
 
 template <class X, class O>
 hipError_t launch_rows(const Linear& a, hipStream_t stream) {
+    using std::integral_constant;
     const int64_t tn = (a.n + 15) / 16;
-    const int mt = a.rows > 16 ? 4 : 1;
-    const dim3 grid((uint32_t)((a.rows + 16 * mt - 1) / (16 * mt) * tn));
-    if (mt == 4)
-        S4_LAUNCH((linear_rows_kernel<X, O, 4>), grid, dim3(64 * WAVES), 0, stream, a, (uint32_t)tn);
+    const auto launch = [&](auto mt, auto ahead) {
+        constexpr int MT = decltype(mt)::value;
+        S4_LAUNCH((linear_rows_kernel<X, O, MT, decltype(ahead)::value>), dim3((uint32_t)((a.rows + 16 * MT - 1) / (16 * MT) * tn)),
+                  dim3(64 * WAVES), 0, stream, a, (uint32_t)tn);
+    };
+    const bool one = fp8_pitch(a.k) <= 128 * WAVES;          // block of k a wave
+    const auto rows = [&](auto mt, auto ahead) { one ? launch(mt, integral_constant<int, 1>{}) : launch(mt, ahead); };
+    if (a.rows <= 16)
+        rows(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    else if (a.rows <= 32)
+        rows(integral_constant<int, 2>{}, integral_constant<int, 2>{});
     else
-        S4_LAUNCH((linear_rows_kernel<X, O, 1>), grid, dim3(64 * WAVES), 0, stream, a, (uint32_t)tn);
+        rows(integral_constant<int, 4>{}, integral_constant<int, std::is_same_v<X, uint8_t> ? 2 : 1>{});
     return hipGetLastError();
 }
 
@@ -452,25 +499,35 @@ hipError_t launch_tiles(const Linear& a, const TilePlan& p, float* parts, hipStr
     S4_LAUNCH((linear_tile_kernel<EXACT, T, O>), dim3((uint32_t)(p.tiles_m * p.tiles_n * p.splits)), dim3(256),
               S::LDS_BYTES, stream, a, p, p.splits > 1 ? parts : nullptr);
     if (p.splits > 1) {
-        const dim3 grid((uint32_t)std::min<int64_t>((a.rows * a.n + 255) / 256, 4096));
-        S4_LAUNCH(linear_join_kernel<O>, grid, dim3(256), 0, stream, a, (const float*)parts, p.splits);
+        const bool four = a.n % 4 == 0;
+        const dim3 grid((uint32_t)std::min<int64_t>((a.rows * a.n + (four ? 1023 : 255)) / (four ? 1024 : 256), 4096));
+        if (four)
+            S4_LAUNCH((linear_join_kernel<O, 4>), grid, dim3(256), 0, stream, a, (const float*)parts, p.splits);
+        else
+            S4_LAUNCH((linear_join_kernel<O, 1>), grid, dim3(256), 0, stream, a, (const float*)parts, p.splits);
     }
     return hipGetLastError();
 }
 
-// X is quantised into the workspace, unless it is quantised already or its few rows are within the product.
-bool quantise_first(const LinearPlan& p, int64_t rows, bool x_quantised) {
-    return !x_quantised && (p.way != Way::ROWS || rows > 16);
+// X is quantised into the workspace, unless it is quantised already or its few rows are within the product:
+// each of the n / 16 workgroups does that again, beside its reads of W.
+bool quantise_first(const LinearPlan& p, const Linear& a, bool x_quantised) {
+    if (x_quantised) return false;
+    return p.tile != 0 || (a.rows > 16 && (a.n > 8192 || a.k > 2048));
 }
 
 }  // namespace
 
 size_t linear_workspace_bytes(shampoo4_dtype out_dtype, int64_t rows, int64_t n, int64_t k, bool x_quantised) {
     const LinearPlan p = linear_plan(out_dtype != SHAMPOO4_BF16, rows, n, k);
+    Linear a{};
+    a.rows = rows;
+    a.n = n;
+    a.k = k;
     size_t bytes = 0;
-    if (quantise_first(p, rows, x_quantised))
+    if (quantise_first(p, a, x_quantised))
         bytes = up256((size_t)(rows * fp8_pitch(k))) + up256((size_t)(rows * fp8_scale_pitch(k)));
-    if (p.way != Way::ROWS && p.tile.splits > 1) bytes += up256((size_t)p.tile.splits * rows * n * 4);
+    if (p.tile && p.plan.splits > 1) bytes += up256((size_t)p.plan.splits * rows * n * 4);
     return bytes;
 }
 
@@ -480,7 +537,7 @@ hipError_t launch_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, const L
     Linear a = given;
     const LinearPlan p = linear_plan(out_dtype != SHAMPOO4_BF16, a.rows, a.n, a.k);
     uint8_t* ws = (uint8_t*)workspace;
-    if (quantise_first(p, a.rows, !a.x)) {
+    if (quantise_first(p, a, !a.x)) {
         uint8_t* scales = ws + up256((size_t)(a.rows * fp8_pitch(a.k)));
         const hipError_t e = launch_fp8_store(dtype, a.rows, a.k, a.x, a.ldx, ws, scales, stream);
         if (e != hipSuccess) return e;
@@ -493,15 +550,17 @@ hipError_t launch_linear(shampoo4_dtype dtype, shampoo4_dtype out_dtype, const L
     by_type(out_dtype, [&](auto o) {
         using O = decltype(o);
         constexpr bool EXACT = !std::is_same_v<O, __bf16>;
-        if (p.way == Way::ROWS) {
+        if (p.tile == 0) {
             if (!a.x)
                 e = launch_rows<uint8_t, O>(a, stream);
             else
                 by_type(dtype, [&](auto x) { e = launch_rows<decltype(x), O>(a, stream); });
-        } else if (p.way == Way::TILE128) {
-            e = launch_tiles<EXACT, 4, O>(a, p.tile, (float*)ws, stream);
+        } else if (p.tile == 2) {
+            e = launch_tiles<EXACT, 2, O>(a, p.plan, (float*)ws, stream);
+        } else if (p.tile == 4) {
+            e = launch_tiles<EXACT, 4, O>(a, p.plan, (float*)ws, stream);
         } else if constexpr (!EXACT) {
-            e = launch_tiles<false, 8, O>(a, p.tile, (float*)ws, stream);
+            e = launch_tiles<false, 8, O>(a, p.plan, (float*)ws, stream);
         }
     });
     return e;

@@ -465,9 +465,9 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
     if constexpr (PER == 1) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            c.template store<float>(out, i, dw[i]);
-            c.template store<float>(out + cols, i, dp[i]);
-            c.template store<float>(out + 2 * cols, i, dg[i]);
+            if (a.dweight) c.template store<float>(out, i, dw[i]);
+            if (a.dpost) c.template store<float>(out + cols, i, dp[i]);
+            if (!TOKEN && a.dgate) c.template store<float>(out + 2 * cols, i, dg[i]);
         }
     } else {
         // the waves' sums, wave by wave
@@ -489,22 +489,27 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
     }
 }
 
-// out[k][c] = sum over groups of parts[group][k][c], in four runs of groups that are added in order.
+// out[k][c] = sum over groups of parts[group][k][c], in sixteen runs of groups that are added in order.
 struct Join {
     float* out[3];
 };
-__global__ __launch_bounds__(256) void block_join_kernel(const float* parts, Join j, int groups, int cols) {
-    __shared__ float run[4][64];
+constexpr int RUNS = 16;
+__global__ __launch_bounds__(64 * RUNS) void block_join_kernel(const float* parts, Join j, int groups, int cols) {
+    __shared__ float run[RUNS][64];
     float* out = j.out[blockIdx.y];
     if (!out) return;
     const int l = threadIdx.x & 63, q = threadIdx.x >> 6, col = blockIdx.x * 64 + l;
     float s = 0.f;
     if (col < cols)
 #pragma unroll 8
-        for (int g = q; g < groups; g += 4) s += ldg(parts + ((int64_t)g * 3 + blockIdx.y) * cols + col);
+        for (int g = q; g < groups; g += RUNS) s += ldg(parts + ((int64_t)g * 3 + blockIdx.y) * cols + col);
     run[q][l] = s;
     __syncthreads();
-    if (q == 0 && col < cols) stg(out + col, ((run[0][l] + run[1][l]) + run[2][l]) + run[3][l]);
+    if (q == 0 && col < cols) {
+#pragma unroll
+        for (int i = 1; i < RUNS; ++i) s += run[i][l];
+        stg(out + col, s);
+    }
 }
 
 // Calls f(waves a row takes, vectors a lane takes).
@@ -593,7 +598,7 @@ hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& give
             });
         });
     if (join)
-        S4_LAUNCH(block_join_kernel, dim3((uint32_t)((a.cols + 63) / 64), 3), dim3(256), 0, stream, a.parts, j, (int)groups,
+        S4_LAUNCH(block_join_kernel, dim3((uint32_t)((a.cols + 63) / 64), 3), dim3(64 * RUNS), 0, stream, a.parts, j, (int)groups,
                   (int)a.cols);
     return hipGetLastError();
 }

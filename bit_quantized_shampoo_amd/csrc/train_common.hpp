@@ -109,6 +109,19 @@ __device__ __forceinline__ typename Vec8<T>::Raw load8_edge(const T* row, int64_
     return r;
 }
 
+// load8_edge in two steps, so that several loads are on their way before the first is waited for: near()
+// loads eight elements inside the row (of at least eight, or element by element), and finish()
+// moves them to their places.
+template <class T>
+__device__ __forceinline__ typename Vec8<T>::Raw load8_near(const T* row, int64_t c, int64_t cols) {
+    return cols >= 8 ? load8(row + min(c, cols - 8)) : load8_edge(row, c, cols);
+}
+template <class T>
+__device__ __forceinline__ void finish8(typename Vec8<T>::Raw& r, int64_t c, int64_t cols) {
+    // by the whole wave: rows mostly end at a vector's end
+    if (cols >= 8 && __any(c + 8 > cols)) r = shift_down<T>(r, (int)min((int64_t)8, max((int64_t)0, c - (cols - 8))));
+}
+
 // The first n (0..8) of eight elements: the whole vector, or pieces of four, two and one.
 template <class T>
 __device__ __forceinline__ void store8_n(T* p, typename Vec8<T>::Raw v, int n) {

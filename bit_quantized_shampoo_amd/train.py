@@ -470,7 +470,9 @@ class Fp8:
     `scales` uint8 [rows / block_rows up, S] (S: P / 128 up to a multiple of 4), the value of element
     (t, c) being codes[t, c] * 2 ** (scales[t // block_rows, c // 128] - 127)."""
 
-    __slots__ = ("codes", "scales", "rows", "cols", "block_rows")
+    # Two tensors, or one buffer with the scales behind the codes (one allocation where a call
+    # makes it), of which codes and scales are views made when asked for.
+    __slots__ = ("_buf", "_codes", "_scales", "rows", "cols", "block_rows")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, block_rows: int = 1):
         if block_rows not in (1, L.FP8_BLOCK):
@@ -482,11 +484,35 @@ class Fp8:
                 raise ValueError(f"{nm} must be a contiguous {dtype} tensor of shape {want}")
         if codes.device != scales.device:
             raise ValueError("codes and scales must be on one device")
-        self.codes, self.scales, self.rows, self.cols, self.block_rows = codes, scales, rows, cols, block_rows
+        self._buf, self._codes, self._scales = None, codes, scales
+        self.rows, self.cols, self.block_rows = rows, cols, block_rows
+
+    @property
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:
+            r, p = self.padded(self.rows, self.cols, self.block_rows)[0]
+            self._codes = self._buf[:r * p].view(_E4M3).view(r, p)
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            (r, p), shape = self.padded(self.rows, self.cols, self.block_rows)
+            self._scales = self._buf[r * p:].view(shape)
+        return self._scales
 
     @property
     def device(self) -> torch.device:
-        return self.codes.device
+        return self._held().device
+
+    def _held(self) -> torch.Tensor:
+        return self._codes if self._buf is None else self._buf
+
+    def _pointers(self):
+        if self._buf is None:
+            return self._codes.data_ptr(), self._scales.data_ptr()
+        p = self._buf.data_ptr()
+        return p, p + self.rows * (-(-self.cols // 128) * 128)
 
     @staticmethod
     def padded(rows: int, cols: int, block_rows: int = 1):
@@ -501,13 +527,15 @@ class Fp8:
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        (r, p), (sr, sp) = self.padded(self.rows, self.cols, self.block_rows)
+        return r * p + sr * sp
 
 
 def _new_fp8(like: torch.Tensor, rows: int, cols: int, block_rows: int) -> Fp8:
+    """Fp8.empty on a tensor's device."""
     a = Fp8.__new__(Fp8)
-    codes, scales = Fp8.padded(rows, cols, block_rows)
-    a.codes, a.scales = like.new_empty(codes, dtype=_E4M3), like.new_empty(scales, dtype=_U8)
+    a._buf = like.new_empty(rows * (-(-cols // 128) * 128) + -(-rows // block_rows) * (-(-cols // 512) * 4), dtype=_U8)
+    a._codes = a._scales = None
     a.rows, a.cols, a.block_rows = rows, cols, block_rows
     return a
 
@@ -520,9 +548,9 @@ def _fp8(a, what: str, rows, cols, block_rows: int, device):
         raise ValueError(f"{what} must have blocks of {block_rows} rows, got {a.block_rows}")
     if (rows is not None and a.rows != rows) or (cols is not None and a.cols != cols):
         raise ValueError(f"{what} must hold {(rows, cols)}, got {(a.rows, a.cols)}")
-    if a.codes.device != device:
-        raise ValueError(f"{what} must be on {device}, got {a.codes.device}")
-    return a.codes.data_ptr(), a.scales.data_ptr()
+    if a.device != device:
+        raise ValueError(f"{what} must be on {device}, got {a.device}")
+    return a._pointers()
 
 
 @_on_stream
@@ -567,19 +595,20 @@ def fp8_load(a: Fp8, dtype=torch.bfloat16, out: torch.Tensor | None = None) -> t
     """The values of a quantised matrix, in `dtype` (or in `out`, of its own type)."""
     if not isinstance(a, Fp8):
         raise TypeError("a must be an Fp8")
-    rows, cols = a.rows, a.cols
-    dev = a.codes.device
+    rows, cols, held = a.rows, a.cols, a._held()
+    dev = held.device
     s = _stream(dev)
+    c, e = a._pointers()
     if out is None:
         if dtype not in _DTYPES:
             raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-        out = a.codes.new_empty((rows, cols), dtype=dtype)
+        out = held.new_empty((rows, cols), dtype=dtype)
         ld = cols
     else:
         ld = _matrix(out, "out", None, rows, cols, dev)
         dtype = out.dtype
-    L.check(L.lib().shampoo4_fp8_load(_DTYPES[dtype], rows, cols, a.block_rows, a.codes.data_ptr(), a.scales.data_ptr(),
-                                      out.data_ptr(), ld, s), "shampoo4_fp8_load")
+    L.check(L.lib().shampoo4_fp8_load(_DTYPES[dtype], rows, cols, a.block_rows, c, e, out.data_ptr(), ld, s),
+            "shampoo4_fp8_load")
     return out
 
 
@@ -594,7 +623,8 @@ def fp8_linear(x, w8: Fp8, out: torch.Tensor | None = None, accumulate: bool = F
     of its eight neighbours (at most a quarter of bfloat16's rounding); those of a float32 or float16
     result are exact, with float32 sums, at half the rate."""
     if isinstance(x, Fp8):
-        rows, k, dev, held = x.rows, x.cols, x.codes.device, x.codes
+        rows, k, held = x.rows, x.cols, x._held()
+        dev = held.device
         s = _stream(dev)
         xc, xe = _fp8(x, "x", None, None, 1, dev)
         xp = ld = 0
@@ -719,7 +749,7 @@ def block_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, h: t
         rr = stats.data_ptr() + 4 * rows
         if save8:
             y8 = _new_fp8(x, rows, cols, 1)
-            yc, ye = y8.codes.data_ptr(), y8.scales.data_ptr()
+            yc, ye = y8._pointers()
     elif y is not None or save8 or h is None:
         raise ValueError("y and save8 need weight, and so does a call without h")
     cfg = L.BlockNormConfig(eps, residual_scale, _dropout_config(p, seed, offset, counter, dev))
@@ -752,6 +782,7 @@ def block_norm_backward(dy: torch.Tensor | None, dres: torch.Tensor | None, x: t
         ldr = _matrix(dres, "dres", dtype, rows, cols, dev)
         rp = dres.data_ptr()
     dweight = dpost = dgate = None
+    sums = x.new_empty((3, cols), dtype=_F32).unbind(0)      # of the vectors' gradients
     if weight is not None:
         if dy is None:
             raise ValueError("weight needs dy")
@@ -759,7 +790,7 @@ def block_norm_backward(dy: torch.Tensor | None, dres: torch.Tensor | None, x: t
         yp = dy.data_ptr()
         wp = _vector(weight, cols, "weight", _F32, dev)
         rr = stats.data_ptr() + 4 * rows
-        dweight = x.new_empty(cols, dtype=_F32)
+        dweight = sums[0]
         dwp = dweight.data_ptr()
     elif dy is not None:
         raise ValueError("dy needs weight")
@@ -772,10 +803,10 @@ def block_norm_backward(dy: torch.Tensor | None, dres: torch.Tensor | None, x: t
         if post_weight is not None:
             pp = _vector(post_weight, cols, "post_weight", _F32, dev)
             hr = stats.data_ptr()
-            dpost = x.new_empty(cols, dtype=_F32)
+            dpost = sums[1]
             dpp = dpost.data_ptr()
         if gate is not None:
-            dgate, lddg = x.new_empty((rows, cols) if grows else cols, dtype=dtype if grows else _F32), cols
+            dgate, lddg = x.new_empty((rows, cols)) if grows else sums[2], cols
             dgp = dgate.data_ptr()
         dh, ldh2 = _out(dh, "dh", x)
         dhp = dh.data_ptr()
