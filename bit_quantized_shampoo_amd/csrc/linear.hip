@@ -288,7 +288,10 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
     const auto product = [&](int stage, int n, int m) {
         const Frag &w = fw[stage & 1][n], &x = fx[m];
         if constexpr (!EXACT) {
-            // as written: left to itself the compiler finds no place for these sums and operands in 512 registers
+            // As written: left to itself the compiler finds no place for these sums and operands in 512 registers.  It
+            // does not know what this is, so the two states that an operand written by a vector instruction just
+            // before needs (the scales may be; codes come from LDS as they are) are taken at their first use.
+            if (n == 0) asm volatile("s_nop 1" ::"v"(we[stage & 1]), "v"(xe[m]));
             asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
                          : "+a"(acc[n][m])
                          : "v"(operand(w)), "v"(operand(x)), "v"(we[stage & 1]), "v"(xe[m]));

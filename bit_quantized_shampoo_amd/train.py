@@ -468,7 +468,8 @@ class Fp8:
     """A [rows, cols] matrix in e4m3 with a scale for each block of 128 columns of `block_rows` rows (1:
     activations, 128: weights): `codes` float8_e4m3fn [rows, P] (P: cols up to a multiple of 128) and
     `scales` uint8 [rows / block_rows up, S] (S: P / 128 up to a multiple of 4), the value of element
-    (t, c) being codes[t, c] * 2 ** (scales[t // block_rows, c // 128] - 127)."""
+    (t, c) being codes[t, c] * 2 ** (scales[t // block_rows, c // 128] - 127).  Columns of padding hold code
+    0, and their scales 1."""
 
     # Two tensors, or one buffer with the scales behind the codes (one allocation where a call
     # makes it), of which codes and scales are views made when asked for.

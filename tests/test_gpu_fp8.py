@@ -200,7 +200,9 @@ def test_linear_large_tiles(out_dt):
     """Sizes that take the largest tiles, whole and ragged, and sums split over long rows."""
     require_gpu()
     rng = np.random.default_rng(12)
-    for t, n, k in ((2048, 2048, 256), (2049, 2500, 200), (4100, 4097, 1153), (256, 256, 8192), (700, 300, 16400)):
+    # 128 x 128 tiles (two), 256 x 256 (three, an odd number of blocks of k among them), ranges of k
+    for t, n, k in ((2048, 2048, 256), (2049, 2500, 200), (4096, 4096, 1100), (4095, 4090, 1153), (3841, 4000, 4000),
+                    (256, 256, 8192), (700, 300, 16400)):
         x = torch.randn(t, k, device="cuda").to(DT[out_dt])
         w = torch.randn(n, k, device="cuda") * 0.05
         _check_linear(x, w, out_dt, True, base=torch.randn(t, n, device="cuda").to(DT[out_dt]), pad=1)
@@ -232,6 +234,21 @@ def test_linear_scales(t, out_dt):
     bad[2] = True
     bad[:, 128:256] = True
     assert torch.equal(torch.isnan(y), bad)
+
+
+def test_linear_not_finite_on_the_largest_tiles():
+    require_gpu()
+    from bit_quantized_shampoo_amd import fp8_linear, fp8_store, fp8_store_weight
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x, w = torch.randn(4000, 1160, generator=g, device="cuda"), torch.randn(4090, 1160, generator=g, device="cuda")
+    want = fp8_linear(fp8_store(x), fp8_store_weight(w), dtype=torch.bfloat16)
+    x[3999, 1159], w[256, 0] = float("inf"), float("nan")
+    announce("fp8 linear with NaN on the largest tiles")
+    y = fp8_linear(fp8_store(x), fp8_store_weight(w), dtype=torch.bfloat16)
+    bad = torch.zeros(4000, 4090, dtype=torch.bool, device="cuda")
+    bad[3999] = True
+    bad[:, 256:384] = True
+    assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], want[~bad])
 
 
 def test_linear_does_not_depend_on_other_rows():
