@@ -106,8 +106,8 @@ bool linear_shape_ok(int64_t rows, int64_t n, int64_t k) {
 }
 
 bool block_shape_ok(int64_t rows, int64_t cols) {
-    // a row takes up to 256 threads, 512 from 4097 columns on, 1024 from 8193 on
-    const int64_t most = int64_t(1) << (cols > 8192 ? 22 : cols > 4096 ? 23 : 24);
+    // a row takes up to 256 threads, 512 from 2049 columns on, 1024 from 4097 on
+    const int64_t most = int64_t(1) << (cols > 4096 ? 22 : cols > 2048 ? 23 : 24);
     return rows >= 0 && rows < most && cols >= 1 && cols <= SHAMPOO4_BLOCK_NORM_COLS;
 }
 

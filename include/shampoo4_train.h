@@ -297,7 +297,7 @@ SHAMPOO4_API shampoo4_status shampoo4_dropout(const shampoo4_dropout_config* cfg
  * and h_rstd NULL.  out may be x or h itself, and y may be h, each with its leading dimension.
  * eps: at least 1e-30, finite.  Finite rows of any size have their norm (squares beyond fp32 are taken
  * of the row divided by a power of two).
- * ESHAPE: cols above 16384, or 2^24 rows or more (2^23 from 4097 columns on, 2^22 from 8193 on). */
+ * ESHAPE: cols above 16384, or 2^24 rows or more (2^23 from 2049 columns on, 2^22 from 4097 on). */
 #define SHAMPOO4_BLOCK_NORM_COLS 16384
 typedef struct {
     float eps, residual_scale;

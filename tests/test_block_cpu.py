@@ -133,6 +133,9 @@ def test_block_forward_refusals():
     assert call(dtype=8) == L.EINVAL and call(grows=2) == L.EINVAL
     assert call(cols=0) == L.ESHAPE and call(cols=16385) == L.ESHAPE and call(rows=1 << 24) == L.ESHAPE
     assert call(rows=-1) == L.ESHAPE
+    for cols, most in ((2048, 1 << 24), (2049, 1 << 23), (4096, 1 << 23), (4097, 1 << 22)):      # of one launch
+        wide = dict(cols=cols, ldx=cols, ldh=cols, ldo=cols, ldy=cols)
+        assert call(**wide, rows=most) == L.ESHAPE and call(**wide, rows=most - 1, x=None) == L.EINVAL
     for k in ("ldx", "ldh", "ldo", "ldy"):
         assert call(**{k: 7}) == L.ESHAPE, k
     assert call(grows=1, ldg=7) == L.ESHAPE and call(grows=1, ldg=8, gate=None) == L.EINVAL
