@@ -12,7 +12,7 @@ namespace {
 constexpr int ROWS = 4;
 
 template <class T>
-__global__ __launch_bounds__(256) void dropout_kernel(const T* __restrict__ x, int64_t ldx, T* y, int64_t ldy,
+__global__ __launch_bounds__(256) void dropout_kernel(const T* x, int64_t ldx, T* y, int64_t ldy,
                                                       int64_t rows, int64_t cols, uint32_t tiles_n, int64_t ntiles,
                                                       Drop d) {
     const uint32_t tile = blockIdx.x * 4 + (threadIdx.x >> 6);

@@ -14,20 +14,27 @@ struct Drop {
     const uint64_t* counter;  // or NULL
 };
 
-// offset + counter, read once a thread
+// offset + counter, read once; in scalar registers, as it is the same for every lane
 __device__ __forceinline__ uint64_t drop_call(const Drop& d) {
-    return d.offset + (d.threshold && d.counter ? ldg(d.counter) : 0);
+    const uint64_t c = d.threshold && d.counter ? ldg(d.counter) : 0;
+    return d.offset + ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(c >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)c));
 }
 
+// a ^ b ^ c in one instruction (its table of results is that of xor)
+__device__ __forceinline__ uint32_t xor3(uint32_t a, uint32_t b, uint32_t c) {
+    return __builtin_amdgcn_bitop3_b32(a, b, c, 0xf0 ^ 0xcc ^ 0xaa);
+}
 __device__ __forceinline__ u32x4 philox(uint32_t x0, uint32_t x1, uint64_t call, uint64_t seed) {
     uint32_t x2 = (uint32_t)call, x3 = (uint32_t)(call >> 32);
     uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+    asm volatile("" : "+s"(k0), "+s"(k1));                   // the rounds' keys are added up again, not kept over a loop
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t a = (uint64_t)x0 * 0xd2511f53u, b = (uint64_t)x2 * 0xcd9e8d57u;
-        x0 = (uint32_t)(b >> 32) ^ x1 ^ k0;
+        x0 = xor3((uint32_t)(b >> 32), x1, k0);
         x1 = (uint32_t)b;
-        x2 = (uint32_t)(a >> 32) ^ x3 ^ k1;
+        x2 = xor3((uint32_t)(a >> 32), x3, k1);
         x3 = (uint32_t)a;
         k0 += 0x9e3779b9u;
         k1 += 0xbb67ae85u;
