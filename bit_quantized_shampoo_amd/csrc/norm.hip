@@ -5,6 +5,11 @@
 // A row is held in registers by one wave or by the waves of a workgroup, as it lies in memory (raw
 // 16-bit values stay packed), so every input is read once; the row's sums go across lanes without LDS
 // and across waves through it.
+//
+// Bytes bound both.  16384 x 4096 bf16, all options, dropout 0.1: forward 140 us, backward 191, without dropout
+// 119 and 164, where a copy of as many bytes takes 105 and 157.  Dropout's generator, 20 wide multiplications for
+// eight columns, is most of that difference: it runs while the row is on its way, but with the row's other
+// arithmetic it is about as long as the row's loads.
 #include <algorithm>
 #include <type_traits>
 
@@ -84,10 +89,10 @@ struct Row {
 // pointers are in scalar registers), columns by 32-bit offsets.
 template <int THREADS, int VPT>
 struct Cols {
-    int cols, t;
+    int cols, t, col0;        // columns of the row, the thread, the first column of all threads
     bool whole;               // rows of whole vectors
-    __device__ __forceinline__ Cols(int cols_, int t_) : cols(cols_), t(t_), whole((cols_ & 7) == 0) {}
-    __device__ __forceinline__ int at(int i) const { return (t + i * THREADS) * 8; }
+    __device__ __forceinline__ Cols(int cols_, int t_, int col0_ = 0) : cols(cols_), t(t_), col0(col0_), whole((cols_ & 7) == 0) {}
+    __device__ __forceinline__ int at(int i) const { return col0 + (t + i * THREADS) * 8; }
     __device__ __forceinline__ int n(int i) const { return max(0, min(8, cols - at(i))); }
 
     // No load is under a lane's own condition: a vector past the row's end is loaded eight from it.  What was
@@ -271,16 +276,18 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
     }
 }
 
-// With sixteen waves (128 registers a lane) a row does not stay in registers beside its sums: it is read
-// again, from L2.
-template <class T, int WPR, int VPT, bool DROP, bool TOKEN>
+// A whole pass (WHOLE), or, for rows of more than BLOCK_WIDE columns, two: the rows' two sums (SUMS), and the rest by
+// ranges of columns, with those sums given (REST).  Registers hold a row of 8192 columns with its sums over rows, 16
+// vectors' worth a lane; one more is spilled, and 4096 x 16384 bf16 in one pass took 2940 us, in two 290-296.
+enum Pass { WHOLE, SUMS, REST };
+template <class T, int WPR, int VPT, bool DROP, bool TOKEN, Pass PASS = WHOLE>
 __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(BlockBackward a, Drop d) {
     constexpr int THREADS = 64 * WPR, PER = rows_of(WPR);
-    constexpr bool AGAIN = WPR > 8, AHEAD = VPT == 1;
+    constexpr bool AGAIN = PASS == SUMS, AHEAD = VPT == 1;   // a vector at a time; the next row beside this one
     __shared__ float red[6][WPR];
     const int t = threadIdx.x % THREADS, cols = (int)a.cols;
     const Row<WPR> sums{red, t >> 6};
-    const Cols<THREADS, VPT> c(cols, t);
+    const Cols<THREADS, VPT> c(cols, t, PASS == REST ? (int)blockIdx.y * (THREADS * VPT * 8) : 0);
     using Raw = typename Vec8<T>::Raw;
     const Rows rows = rows_here<WPR>();
     const float inv = 1.f / (float)cols;
@@ -321,9 +328,10 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
     const float drop_scale = DROP ? d.scale : 1.f;
     const float* gate = TOKEN ? nullptr : (const float*)a.gate;
     const auto shared = [&](int i) {
-        const u32x8 w = c.shared(a.weight, i), p = c.shared(a.post, i), g = c.shared(gate, i);
-        return Shared{c.finish_shared(a.weight, w, i), c.finish_shared(a.post, p, i),
-                      c.finish_shared(gate, g, i) * (TOKEN ? 1.f : drop_scale)};
+        const float *pw = a.weight, *pp = a.post, *pg = gate;
+        if (AGAIN) asm volatile("" : "+s"(pw), "+s"(pp), "+s"(pg));      // not kept from one row for the next
+        const u32x8 w = c.shared(pw, i), p = c.shared(pp, i), g = c.shared(pg, i);
+        return Shared{c.finish_shared(pw, w, i), c.finish_shared(pp, p, i), c.finish_shared(pg, g, i) * (TOKEN ? 1.f : drop_scale)};
     };
     In now[AGAIN ? 1 : VPT], next[AHEAD ? VPT : 1];
     Factors f_now = {}, f_next = {};
@@ -335,15 +343,19 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
     if (!AGAIN)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) vec[i] = shared(i);
-    floatx8 dw[VPT] = {}, dp[VPT] = {}, dg[VPT] = {};
+    // A vector gate and the weight behind the block share one sum, da = sum drop(g) hh: dgate = da post, dpost = da gate.
+    floatx8 dw[VPT] = {}, da[VPT] = {};
     int set = 0;
     for (int64_t r = rows.first; r < a.rows; r += rows.stride, set ^= 3) {
         const int64_t row = here(r);
-        Keep keep[DROP ? VPT : 1];
+        Keep keep[DROP && !AGAIN ? VPT : 1];
         const auto numbers = [&]() {                         // while the row is on its way
             if (DROP)
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) keep[i] = drop_keep8(d, call, row, c.at(i) >> 3);
+                for (int i = 0; i < VPT; ++i) {
+                    keep[i] = drop_keep8(d, call, row, c.at(i) >> 3);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             __builtin_amdgcn_sched_barrier(0);
         };
         if constexpr (AHEAD) {
@@ -361,20 +373,22 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
             if (!AGAIN)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) now[i] = load(row, i);
-            numbers();
-            if (!AGAIN)
+            if constexpr (!AGAIN) {
+                numbers();
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) finish(now[i], i);
+            }
         }
         const float rx = f_now.x, hr = f_now.h;
         // One reduction for both norms: mean(u hh) = sum q (dres + rstd (t - xh s)) is linear in s = mean(t xh), with
         // q = drop(gate post) hh the same for every term.
         float s = 0.f, qa = 0.f, qb = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
+#pragma unroll(AGAIN ? 1 : VPT)
+        for (int i = 0; i < (PASS == REST ? 0 : VPT); ++i) {
             if (AGAIN) {
                 now[0] = load(row, i);
                 vec[0] = shared(i);
+                if (DROP) keep[0] = drop_keep8(d, call, row, c.at(i) >> 3);
                 finish(now[0], i);
             }
             In& in = now[AGAIN ? 0 : i];
@@ -388,7 +402,7 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
                     q *= Vec8<T>::get(in.g);
                 else
                     q *= v.g;
-                if (DROP) q = drop8(q, keep[i], d);
+                if (DROP) q = drop8(q, keep[AGAIN ? 0 : i], d);
                 const floatx8 dr = Vec8<T>::get(in.dr);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
@@ -401,23 +415,32 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
             unpack_again(in.dr);
             unpack_again(in.h);
             unpack_again(in.g);
+            if (DROP) unpack_again(keep[AGAIN ? 0 : i].w);
             if (VPT > 1) __builtin_amdgcn_sched_barrier(0);
         }
-        s = sums.partial(s, set);
-        if (a.post) {
-            qa = sums.partial(qa, set + 1);
-            qb = sums.partial(qb, set + 2);
+        float s2 = 0.f;
+        if constexpr (PASS == REST) {
+            s = ldg(a.sums + 2 * row);
+            s2 = ldg(a.sums + 2 * row + 1);
+        } else {
+            s = sums.partial(s, set);
+            if (a.post) {
+                qa = sums.partial(qa, set + 1);
+                qb = sums.partial(qb, set + 2);
+            }
+            sums.meet();
+            s = sums.total(s, set) * inv * rx;               // rstd mean(t xh), and h_rstd mean(u hh)
+            if (a.post) s2 = (sums.total(qa, set + 1) - s * sums.total(qb, set + 2)) * inv * (TOKEN ? hr * drop_scale : hr);
         }
-        sums.meet();
-        s = sums.total(s, set) * inv * rx;                   // rstd mean(t xh)
-        const float s2 = a.post ? (sums.total(qa, set + 1) - s * sums.total(qb, set + 2)) * inv * (TOKEN ? hr * drop_scale : hr) : 0.f;
+        if constexpr (PASS == SUMS) {
+            if (t == 0) {
+                stg(a.sums + 2 * row, s);
+                stg(a.sums + 2 * row + 1, s2);
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (AGAIN) {
-                now[0] = load(row, i);
-                vec[0] = shared(i);
-                finish(now[0], i);
-            }
             const In& in = now[AGAIN ? 0 : i];
             const Shared& v = vec[AGAIN ? 0 : i];
             const floatx8 xh = Vec8<T>::get(in.x) * rx, y = Vec8<T>::get(in.dy);
@@ -429,45 +452,39 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
             }
             if (a.dx) c.template store<T>((T*)a.dx + row * a.lddx, i, gx * a.rho);
             if (a.h) {
-                const floatx8 hh = Vec8<T>::get(in.h) * hr;
-                floatx8 z = hh * v.p;                        // what the gate multiplies
+                floatx8 hh = Vec8<T>::get(in.h) * hr;
                 if (DROP) {
                     gx = drop8(gx, keep[i], d);              // dropped: no gradient
-                    if (!a.post) z = drop8(z, keep[i], d);   // and h may be anything
+                    if (!a.post) hh = drop8(hh, keep[i], d); // and h may be anything
                 }
                 if (TOKEN) {
                     gx *= drop_scale;
-                    if (a.dgate) c.template store<T>((T*)a.dgate + row * a.lddgate, i, gx * z);
+                    if (a.dgate) c.template store<T>((T*)a.dgate + row * a.lddgate, i, gx * (hh * v.p));
                     gx *= Vec8<T>::get(in.g);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dg[i][j] = fmaf(gx[j], z[j], dg[i][j]);
-                    gx *= v.g;
                 }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) da[i][j] = fmaf(gx[j], hh[j], da[i][j]);
+                if (!TOKEN) gx *= v.g;
                 if (a.post) {
                     // dh = rstd (u - hh mean(u hh))
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        dp[i][j] = fmaf(gx[j], hh[j], dp[i][j]);
-                        gx[j] = fmaf(gx[j] * v.p[j], hr, -hh[j] * s2);
-                    }
+                    for (int j = 0; j < 8; ++j) gx[j] = fmaf(gx[j] * v.p[j], hr, -hh[j] * s2);
                 }
                 if (a.dh) c.template store<T>((T*)a.dh + row * a.lddh, i, gx);
             }
             if (VPT > 1) __builtin_amdgcn_sched_barrier(0);  // one vector's values at a time in registers
         }
     }
-    if (!a.parts) return;
-    if (DROP)
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) dg[i] *= drop_scale;
+    if (PASS == SUMS || !a.parts) return;
+    const auto dp = [&](int i) { return TOKEN ? da[i] : da[i] * vec[i].g; };
+    const auto dg = [&](int i) { return da[i] * (vec[i].p * drop_scale); };
     float* out = a.parts + (int64_t)blockIdx.x * 3 * cols;
     if constexpr (PER == 1) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (a.dweight) c.template store<float>(out, i, dw[i]);
-            if (a.dpost) c.template store<float>(out + cols, i, dp[i]);
-            if (!TOKEN && a.dgate) c.template store<float>(out + 2 * cols, i, dg[i]);
+            if (a.dpost) c.template store<float>(out + cols, i, dp(i));
+            if (!TOKEN && a.dgate) c.template store<float>(out + 2 * cols, i, dg(i));
         }
     } else {
         // the waves' sums, wave by wave
@@ -475,14 +492,16 @@ __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(Bloc
         for (int k = 0; k < PER; ++k) {
             if ((int)(threadIdx.x >> 6) == k)
 #pragma unroll
-                for (int i = 0; i < VPT; ++i)
+                for (int i = 0; i < VPT; ++i) {
+                    const floatx8 p = dp(i), g = dg(i);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const int at = c.at(i) + j;
                         all[0][at] = k ? all[0][at] + dw[i][j] : dw[i][j];
-                        all[1][at] = k ? all[1][at] + dp[i][j] : dp[i][j];
-                        all[2][at] = k ? all[2][at] + dg[i][j] : dg[i][j];
+                        all[1][at] = k ? all[1][at] + p[j] : p[j];
+                        all[2][at] = k ? all[2][at] + g[j] : g[j];
                     }
+                }
             __syncthreads();
         }
         for (int i = threadIdx.x; i < 3 * cols; i += 64 * PER) stg(out + i, all[i / cols][i % cols]);
@@ -512,15 +531,13 @@ __global__ __launch_bounds__(64 * RUNS) void block_join_kernel(const float* part
     }
 }
 
-// Calls f(waves a row takes, vectors a lane takes).
+// Calls f(waves a row takes, vectors a lane takes).  Backward, up to BLOCK_WIDE columns.
 template <bool FORWARD, class F>
 void by_row(int64_t cols, F f) {
     constexpr std::integral_constant<int, 1> one{};
     constexpr std::integral_constant<int, 2> two{};
-    constexpr std::integral_constant<int, 3> three{};
     constexpr std::integral_constant<int, 4> four{};
     constexpr std::integral_constant<int, 8> eight{};
-    constexpr std::integral_constant<int, 12> twelve{};
     constexpr std::integral_constant<int, 16> sixteen{};
     if (cols <= 512) return f(one, one);
     if constexpr (FORWARD) {
@@ -533,8 +550,7 @@ void by_row(int64_t cols, F f) {
         if (cols <= 1024) return f(one, two);
         if (cols <= 2048) return f(two, two);
         if (cols <= 4096) return f(four, two);
-        if (cols <= 8192) return f(eight, two);
-        f(twelve, three);
+        f(eight, two);
     }
 }
 // Calls f(dropout, gate by element).
@@ -549,8 +565,11 @@ void by_form(bool drop, bool token, F f) {
 int64_t workgroups(int64_t rows, int wpr, int64_t most) {
     return std::min<int64_t>((rows + rows_of(wpr) - 1) / rows_of(wpr), most);
 }
+// Backward beyond BLOCK_WIDE: ranges of 4096 columns, by four waves with two vectors a lane.
+int64_t wide_ranges(int64_t cols) { return (cols + 4095) / 4096; }
 // Of the backward kernel: eight waves a CU, each with a fixed set of rows whose sums it keeps.
 int64_t back_groups(int64_t rows, int64_t cols) {
+    if (cols > BLOCK_WIDE) return workgroups(rows, 4, 512 / wide_ranges(cols));
     int64_t n = 0;
     by_row<false>(cols, [&](auto w, auto) {
         constexpr int W = decltype(w)::value;
@@ -577,16 +596,28 @@ hipError_t launch_block_forward(shampoo4_dtype dtype, const BlockForward& a, con
 }
 
 size_t block_workspace_bytes(int64_t rows, int64_t cols) {
-    return (size_t)back_groups(rows, cols) * 3 * cols * 4;
+    return (size_t)back_groups(rows, cols) * 3 * cols * 4 + (cols > BLOCK_WIDE ? (size_t)rows * 8 : 0);
 }
 
 hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& given, const Drop& d, hipStream_t stream) {
     BlockBackward a = given;
     const Join j{{a.dweight, a.dpost, a.gate_rows ? nullptr : (float*)a.dgate}};
     const bool join = j.out[0] || j.out[1] || j.out[2];
-    if (!join) a.parts = nullptr;
     const int64_t groups = back_groups(a.rows, a.cols);
-    if (groups > 0)
+    if (a.parts) a.sums = a.parts + groups * 3 * a.cols;
+    if (!join) a.parts = nullptr;
+    if (groups > 0 && a.cols > BLOCK_WIDE)
+        by_type(dtype, [&](auto t) {
+            using T = decltype(t);
+            by_form(d.threshold && a.h, a.gate_rows, [&](auto drop, auto token) {
+                constexpr bool D = decltype(drop)::value, G = decltype(token)::value;
+                S4_LAUNCH((block_backward_kernel<T, 8, 4, D, G, SUMS>), dim3((uint32_t)workgroups(a.rows, 8, 512)),
+                          dim3(threads_of(8)), 0, stream, a, d);
+                S4_LAUNCH((block_backward_kernel<T, 4, 2, D, G, REST>), dim3((uint32_t)groups, (uint32_t)wide_ranges(a.cols)),
+                          dim3(threads_of(4)), 0, stream, a, d);
+            });
+        });
+    else if (groups > 0)
         by_type(dtype, [&](auto t) {
             using T = decltype(t);
             by_row<false>(a.cols, [&](auto w, auto v) {

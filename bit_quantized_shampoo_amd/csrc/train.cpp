@@ -458,10 +458,10 @@ shampoo4_status shampoo4_block_norm_backward(const shampoo4_block_norm_config* c
     if (!aligned(weight, 4) || !aligned(post_weight, 4) || !aligned(rstd, 4) || !aligned(h_rstd, 4) ||
         !aligned(dweight, 4) || !aligned(dpost_weight, 4))
         return SHAMPOO4_EALIGN;
-    if (dweight || dpost_weight || (dgate && !gate_rows))
+    if (dweight || dpost_weight || (dgate && !gate_rows) || cols > BLOCK_WIDE)
         S4_TRY(workspace_ok(workspace, workspace_bytes, block_workspace_bytes(rows, cols)));
     const BlockBackward a{dy, dres, x, h, gate, rstd, weight, h_rstd, post_weight, dx, dh, dgate, dweight, dpost_weight,
-                          (float*)workspace, rows, cols, lddy, lddres, ldx, ldh, ldgate, lddx, lddh, lddgate,
+                          (float*)workspace, nullptr, rows, cols, lddy, lddres, ldx, ldh, ldgate, lddx, lddh, lddgate,
                           cfg->residual_scale, gate_rows};
     return launched(launch_block_backward(dtype, a, d, as_stream(stream)));
 }

@@ -175,11 +175,13 @@ struct BlockBackward {
     void* dgate;
     float* dweight;
     float* dpost;
-    float* parts;
+    float* parts;             // the workspace: sums of groups of rows
+    float* sums;              // behind them, of more than BLOCK_WIDE columns: the rows' two sums (set by the launcher)
     int64_t rows, cols, lddy, lddres, ldx, ldh, ldgate, lddx, lddh, lddgate;
     float rho;
     int gate_rows;
 };
+constexpr int BLOCK_WIDE = 8192;      // columns of a row that one pass holds in registers
 size_t block_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& a, const Drop& d, hipStream_t stream);
 

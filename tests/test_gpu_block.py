@@ -201,6 +201,29 @@ def test_block_many_rows():
     _check(1030, 1032, "bf16", *OPTIONS[0])
 
 
+@pytest.mark.parametrize("t,c,dt,k", [(1, 8193, "f32", 1), (5, 12288, "f16", 5), (4, 12289, "bf16", 4), (3, 16383, "f32", 3),
+                                      (520, 8200, "bf16", 0), (300, 9001, "f32", 2), (140, 16384, "bf16", 1)])
+def test_block_wide_rows(t, c, dt, k):
+    """Rows that the backward pass takes by ranges of columns, their two sums before; more rows than groups."""
+    require_gpu()
+    _check(t, c, dt, *OPTIONS[k], strided=t == 4, dres=t != 5)
+
+
+def test_block_wide_rows_in_place():
+    require_gpu()
+    from bit_quantized_shampoo_amd import block_norm_backward
+    for dt in ("bf16", "f32"):
+        v, kw, (x, _, stats), got = _check(6, 10240, dt, True, "channel", True, 0.1, 0.5)
+        announce(f"wide rows in place {dt}")
+        h, dy, dres = v["h"].clone(), v["dy"].clone(), v["dres"].clone()
+        out = block_norm_backward(dy, dres, x, v["weight"], stats, h=h, dx=dres, dh=h, **kw)
+        assert out[0] is dres and out[1] is h
+        assert all(torch.equal(a, b) for a, b in zip(out, got))
+        dres = v["dres"].clone()
+        out = block_norm_backward(dy, dres, x, v["weight"], stats, h=v["h"], dx=dy, dh=dres, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(out, got))
+
+
 def test_block_rows_beyond_fp32_squares():
     """Rows whose squares leave fp32, and rows of very small values."""
     require_gpu()
