@@ -6,7 +6,7 @@
 // 16-bit values stay packed), so every input is read once; the row's sums go across lanes without LDS
 // and across waves through it.
 //
-// Bytes bound both.  16384 x 4096 bf16, all options, dropout 0.1: forward 140 us, backward 191, without dropout
+// Bytes bound both.  16384 x 4096 bf16, all options, dropout 0.1: forward 133 us, backward 191, without dropout
 // 119 and 164, where a copy of as many bytes takes 105 and 157.  Dropout's generator, 20 wide multiplications for
 // eight columns, is most of that difference: it runs while the row is on its way, but with the row's other
 // arithmetic it is about as long as the row's loads.
@@ -532,7 +532,11 @@ __global__ __launch_bounds__(64 * RUNS) void block_join_kernel(const float* part
 }
 
 // Calls f(waves a row takes, vectors a lane takes).  Backward, up to BLOCK_WIDE columns.
-template <bool FORWARD, class F>
+// Forward, rows of 16-bit values of more than 2048 columns are two vectors a lane: their arithmetic is as long as
+// their loads, and a row's reductions are shared by twice as many (16384 x 4096 bf16 with dropout 133 us where one
+// vector takes 143; 8192 x 8192 124 and 138).  Of fp32, whose elements are half as many, one (8192 x 4096 103 and
+// 108).  Backward, two of every type: it holds its sums over rows in registers, and few waves fit beside them.
+template <class T, bool FORWARD, class F>
 void by_row(int64_t cols, F f) {
     constexpr std::integral_constant<int, 1> one{};
     constexpr std::integral_constant<int, 2> two{};
@@ -543,8 +547,13 @@ void by_row(int64_t cols, F f) {
     if constexpr (FORWARD) {
         if (cols <= 1024) return f(two, one);
         if (cols <= 2048) return f(four, one);
-        if (cols <= 4096) return f(eight, one);
-        if (cols <= 8192) return f(sixteen, one);
+        if constexpr (sizeof(T) == 2) {
+            if (cols <= 4096) return f(four, two);
+            if (cols <= 8192) return f(eight, two);
+        } else {
+            if (cols <= 4096) return f(eight, one);
+            if (cols <= 8192) return f(sixteen, one);
+        }
         f(sixteen, two);
     } else {
         if (cols <= 1024) return f(one, two);
@@ -571,7 +580,7 @@ int64_t wide_ranges(int64_t cols) { return (cols + 4095) / 4096; }
 int64_t back_groups(int64_t rows, int64_t cols) {
     if (cols > BLOCK_WIDE) return workgroups(rows, 4, 512 / wide_ranges(cols));
     int64_t n = 0;
-    by_row<false>(cols, [&](auto w, auto) {
+    by_row<float, false>(cols, [&](auto w, auto) {
         constexpr int W = decltype(w)::value;
         n = workgroups(rows, W, 256 * std::max(1, 8 / (W * rows_of(W))));
     });
@@ -584,7 +593,7 @@ hipError_t launch_block_forward(shampoo4_dtype dtype, const BlockForward& a, con
     if (a.rows <= 0) return hipSuccess;
     by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        by_row<true>(a.cols, [&](auto w, auto v) {
+        by_row<T, true>(a.cols, [&](auto w, auto v) {
             constexpr int W = decltype(w)::value, V = decltype(v)::value;
             by_form(d.threshold && a.h, a.gate_rows, [&](auto drop, auto token) {
                 S4_LAUNCH((block_forward_kernel<T, W, V, decltype(drop)::value, decltype(token)::value>),
@@ -620,7 +629,7 @@ hipError_t launch_block_backward(shampoo4_dtype dtype, const BlockBackward& give
     else if (groups > 0)
         by_type(dtype, [&](auto t) {
             using T = decltype(t);
-            by_row<false>(a.cols, [&](auto w, auto v) {
+            by_row<T, false>(a.cols, [&](auto w, auto v) {
                 constexpr int W = decltype(w)::value, V = decltype(v)::value;
                 by_form(d.threshold && a.h, a.gate_rows, [&](auto drop, auto token) {
                     S4_LAUNCH((block_backward_kernel<T, W, V, decltype(drop)::value, decltype(token)::value>),
