@@ -230,13 +230,12 @@ struct TilePlan {
     int blocks;               // of k, a range's (a multiple of four)
 };
 
-// Range of k and output tile of this workgroup.  Workgroups go to the eight XCDs round robin; each
+// Range of k and output tile number b.  Workgroups go to the eight XCDs round robin; each
 // XCD takes a contiguous range of the tiles (the remainder, under eight, keeps its place), in groups
 // of four tile rows, so that the tiles that one L2 serves share their rows of X and W.
-__device__ __forceinline__ void place(const TilePlan& p, int& split, int& tile_m, int& tile_n) {
-    const int n8 = gridDim.x >> 3;
-    const int b = (int)blockIdx.x < 8 * n8 ? ((int)blockIdx.x & 7) * n8 + ((int)blockIdx.x >> 3) : (int)blockIdx.x;
-    const int tiles = p.tiles_m * p.tiles_n;
+__device__ __forceinline__ void place(const TilePlan& p, int b, int& split, int& tile_m, int& tile_n) {
+    const int tiles = p.tiles_m * p.tiles_n, n8 = (tiles * p.splits) >> 3;
+    if (b < 8 * n8) b = (b & 7) * n8 + (b >> 3);
     split = b / tiles;
     const int t = b - split * tiles;
     const int g = t / (4 * p.tiles_n);
@@ -251,44 +250,56 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
     using S = TileShape<T>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int split, tile_m, tile_n;
-    place(plan, split, tile_m, tile_n);
-    const int64_t m0 = (int64_t)tile_m * S::SIDE, n0 = (int64_t)tile_n * S::SIDE;
     const int64_t pitch = fp8_pitch(a.k), sp = fp8_scale_pitch(a.k);
-    const int nkb = (int)(pitch >> 7), kb0 = split * plan.blocks, kb1 = min(nkb, kb0 + plan.blocks);
+    const int nkb = (int)(pitch >> 7), all = plan.tiles_m * plan.tiles_n * plan.splits;
     const int wm = (wv & 1) * 16 * T, wn = (wv >> 1) * 16 * T;
     const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds;
 
     // waves 0 and 1 load W's rows, 2 and 3 X's
     const bool isx = wv >= 2;
-    const int64_t r0 = isx ? m0 : n0, rows = isx ? a.rows : a.n;
-    const Resource codes = resource((isx ? a.xc : a.wc) + r0 * pitch, min(rows - r0, (int64_t)S::SIDE) * pitch);   // at most 2^31 bytes
+    struct Source {
+        int kb0, kb1;                                        // of blocks of k
+        Resource codes, xscales, wscales;
+    };
+    // Behind the last tile: one of no blocks, whose loads give zeros.
+    const auto source = [&](int t) {
+        Source q{};
+        int split, tile_m, tile_n;
+        place(plan, min(t, all - 1), split, tile_m, tile_n);
+        const int64_t m0 = (int64_t)tile_m * S::SIDE, n0 = (int64_t)tile_n * S::SIDE;
+        q.kb0 = split * plan.blocks;
+        q.kb1 = t < all ? min(nkb, q.kb0 + plan.blocks) : q.kb0;
+        const int64_t r0 = isx ? m0 : n0, rows = isx ? a.rows : a.n;
+        q.codes = resource((isx ? a.xc : a.wc) + r0 * pitch, min(rows - r0, (int64_t)S::SIDE) * pitch);   // at most 2^31 bytes
+        // scales of four blocks of k: 64 rows of X a wave, and the one row of W's that the wave's outputs take
+        q.xscales = resource(a.xs + m0 * sp, (a.rows - m0) * sp);
+        const int64_t wrow = min(n0 + wn, a.n - 1) >> 7;
+        q.wscales = resource(a.ws + wrow * sp, ((a.n + 127) / 128 - wrow) * sp);
+        return q;
+    };
     const int lrow = (wv & 1) * S::LOADS * 8 + (lane >> 3);
     const uint32_t even = (uint32_t)(lrow * pitch + 16 * place_of(lrow, lane & 7));
     const uint32_t odd = (uint32_t)(lrow * pitch + 16 * place_of(lrow + 8, lane & 7));
     const uint32_t to = base + (isx ? S::X : 0) + (wv & 1) * S::LOADS * 1024;
     uint32_t rows8 = (uint32_t)(8 * pitch);
+    Source src = source(blockIdx.x);
     const auto load = [&](int b, int stage, int j) {         // past the last block: zeros, by an offset past the end
         asm volatile("" : "+s"(rows8));                      // added here, not kept in a register for each j
-        const uint32_t v = (j & 1 ? odd : even) + (j * rows8 + (b < kb1 ? 0u : 0x80000000u));
-        load16_lds(to + (stage & 1) * S::STAGE + j * 1024, codes, v, b < kb1 ? 128 * b : 0);
+        const uint32_t v = (j & 1 ? odd : even) + (j * rows8 + (b < src.kb1 ? 0u : 0x80000000u));
+        load16_lds(to + (stage & 1) * S::STAGE + j * 1024, src.codes, v, b < src.kb1 ? 128 * b : 0);
     };
-    // scales of four blocks of k: 64 rows of X a wave, and the one row of W's that the wave's outputs take
-    const Resource xscales = resource(a.xs + m0 * sp, (a.rows - m0) * sp);
-    const int64_t wrow = min(n0 + wn, a.n - 1) >> 7;
-    const Resource wscales = resource(a.ws + wrow * sp, ((a.n + 127) / 128 - wrow) * sp);
     const uint32_t xvoff = (uint32_t)(min(wv * 64 + lane, S::SIDE - 1) * sp);
-    const auto load_scales = [&](int b) {                    // of block b (a multiple of four) and the three after it
-        const uint32_t k = (uint32_t)min((int64_t)b, sp - 4);
-        const uint32_t slot = base + S::SCALES + ((b >> 2) & 1) * S::SLOT;
-        load4_lds(slot + wv * 256, xscales, xvoff, k);
-        load4_lds(slot + S::SLOT / 2 + wv * 256, wscales, 0, k);
+    const auto load_scales = [&](int b, int slot) {          // of block b (a multiple of four) and the three after it
+        const uint32_t k = (uint32_t)min((int64_t)b, sp - 4), at = base + S::SCALES + slot * S::SLOT;
+        load4_lds(at + wv * 256, src.xscales, xvoff, k);
+        load4_lds(at + S::SLOT / 2 + wv * 256, src.wscales, 0, k);
     };
 
     // A block is two halves, of X's first and last T / 2 operands with all of W's.
     floatx4 acc[T][T] = {};                                  // [n][m]: columns of Y in a lane's registers
     Frag fw[2][T], fx[T];                                    // W's: of this block and of the next
-    uint32_t xe[T], we[2];
+    uint32_t xw[T], ww[2];                                   // scales of four blocks each
+    uint32_t xe = 0, we = 0;                                 // this block's; the matrix instruction takes the lowest byte
     const int row = lane & 15;
     const int at0 = row * 128 + 16 * place_of(row, lane >> 4), at1 = row * 128 + 16 * place_of(row, 4 + (lane >> 4));
     const auto frag = [&](const uint8_t* p, int stage, int i) {
@@ -297,19 +308,19 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
     };
     const auto read_x = [&](int stage, int m) { fx[m] = frag(lds + S::X + wm * 128, stage, m); };
     const auto read_w = [&](int stage, int n) { fw[stage & 1][n] = frag(lds + wn * 128, stage, n); };
-    const auto scale_slot = [&](int b) { return lds + S::SCALES + ((b >> 2) & 1) * S::SLOT + (b & 3); };
-    const auto read_xe = [&](int b, int m) { xe[m] = scale_slot(b)[(wm + 16 * m + row) * 4]; };
-    const auto read_we = [&](int b, int stage) { we[stage & 1] = scale_slot(b)[S::SLOT / 2 + wv * 256]; };
-    const auto product = [&](int stage, int n, int m) {
+    const auto read_xe = [&](int slot, int m) { xw[m] = *(const uint32_t*)(lds + S::SCALES + slot * S::SLOT + (wm + 16 * m + row) * 4); };
+    const auto read_we = [&](int slot, int stage) { ww[stage & 1] = *(const uint32_t*)(lds + S::SCALES + slot * S::SLOT + S::SLOT / 2 + wv * 256); };
+    const auto product = [&](int stage, int n, int m, int sh) {
         const Frag &w = fw[stage & 1][n], &x = fx[m];
+        if (n == 0) xe = xw[m] >> sh;
         if constexpr (!EXACT) {
             // As written: left to itself the compiler finds no place for these sums and operands in 512 registers.  It
             // does not know what this is, so the two states that an operand written by a vector instruction just
-            // before needs (the scales may be; codes come from LDS as they are) are taken at their first use.
-            if (n == 0) asm volatile("s_nop 1" ::"v"(we[stage & 1]), "v"(xe[m]));
+            // before needs (the scales are; codes come from LDS as they are) are taken at their first use.
+            if (n == 0) asm volatile("s_nop 1" ::"v"(we), "v"(xe));
             asm volatile("v_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]"
                          : "+a"(acc[n][m])
-                         : "v"(operand(w)), "v"(operand(x)), "v"(we[stage & 1]), "v"(xe[m]));
+                         : "v"(operand(w)), "v"(operand(x)), "v"(we), "v"(xe));
         } else {
             floatx4 s = {};
 #pragma unroll
@@ -317,110 +328,162 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
                 s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(q < 2 ? w.lo : w.hi, q & 1), widen(q < 2 ? x.lo : x.hi, q & 1),
                                                             s, 0, 0, 0);
             // the scales' product may leave fp32's range where its product with the sum does not
-            const int shift = (int)(we[stage & 1] + xe[m]) - 254;
-            const float one = we[stage & 1] == 255u || xe[m] == 255u ? __builtin_nanf("") : 1.f;
+            const uint32_t ew = we & 255u, ex = xe & 255u;
+            const int shift = (int)(ew + ex) - 254;
+            const float one = ew == 255u || ex == 255u ? __builtin_nanf("") : 1.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][m][i] = fmaf(__builtin_amdgcn_ldexpf(s[i], shift), one, acc[n][m][i]);
         }
     };
 
-    if (kb0 < kb1) {
-        load_scales(kb0);
+    // Beside the first products of a block the rest of its operands are read; then its place in LDS is free, and
+    // the loads of the block after the next are spread over the products that follow: a CU takes one in
+    // 16 clocks at best (one in 22 when all of them load), and a wave that waits to issue one issues no
+    // product.  Beside the second half the next block's first operands are read.
+    constexpr int STEPS = T * T / 2, FREE = STEPS * 3 / 8, SPREAD = 2 * STEPS - FREE;
+    constexpr int EARLY = ((STEPS - FREE) * S::LOADS + SPREAD - 1) / SPREAD;     // loads of the first half
+    constexpr int NEXT = (3 * T / 2 + STEPS - 1) / STEPS;                        // operands read a step
+    // The largest tiles, whose workgroups have a CU alone, are taken one after the other by 256 of them: the last
+    // blocks of one load the next one's first, and its stores are on their way beside the next one's products.
+    constexpr bool MANY = T == 8;
+    constexpr int STORES = MANY ? T * T / 2 : 0;             // of a wave and whole tile at least
+
+    int number = blockIdx.x, slot = 0;                       // the slot of the scales that are in use
+    load_scales(src.kb0, 0);
 #pragma unroll
-        for (int j = 0; j < S::LOADS; ++j) load(kb0, 0, j);
+    for (int j = 0; j < S::LOADS; ++j) load(src.kb0, 0, j);
 #pragma unroll
-        for (int j = 0; j < S::LOADS; ++j) load(kb0 + 1, 1, j);
-        arrived<S::LOADS>();
+    for (int j = 0; j < S::LOADS; ++j) load(src.kb0 + 1, 1, j);
+    arrived<S::LOADS>();
+    bool storing = false;                                    // the last tile's stores are behind the loads of block 1
+    for (;;) {
+        // read here for every tile: no registers hold them beside the last tile's outputs
 #pragma unroll
         for (int n = 0; n < T; ++n) read_w(0, n);
-        read_we(kb0, 0);
+        read_we(slot, 0);
 #pragma unroll
         for (int m = 0; m < T / 2; ++m) {
             read_x(0, m);
-            read_xe(kb0, m);
+            read_xe(slot, m);
         }
-        // Beside the first products of a block the rest of its operands are read; then its place in LDS is free, and
-        // the loads of the block after the next are spread over the products that follow: a CU takes one in
-        // 16 clocks at best (one in 22 when all of them load), and a wave that waits to issue one issues no
-        // product.  Beside the second half the next block's first operands are read.
-        constexpr int STEPS = T * T / 2, FREE = STEPS * 3 / 8, SPREAD = 2 * STEPS - FREE;
-        constexpr int EARLY = ((STEPS - FREE) * S::LOADS + SPREAD - 1) / SPREAD;     // loads of the first half
-        constexpr int NEXT = (3 * T / 2 + STEPS - 1) / STEPS;                        // operands read a step
-        const auto load_step = [&](int b, int stage, int k) {
-#pragma unroll
-            for (int j = 0; j < S::LOADS; ++j)
-                if (FREE + j * SPREAD / S::LOADS == k) load(b, stage, j);
-        };
-        // Block b, in stage J = b % 2.  Beside an even one the scales of the next four blocks are loaded (twice, as
-        // that takes no branch: over one the compiler moves products past the barriers that they are to cover).
-        const auto block = [&](int b, auto j) {
-            constexpr int J = decltype(j)::value;
-#pragma unroll
-            for (int k = 0; k < STEPS; ++k) {
-                if (k < T / 2) {
-                    read_x(J, T / 2 + k);
-                    read_xe(b, T / 2 + k);
-                }
-                if (k == FREE) {
-                    all_read();
-                    if (J == 0) load_scales((b & ~3) + 4);
-                }
-                load_step(b + 2, J, k);
-                product(J, k % T, k / T);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            // the next block is whole in LDS; only what has just been issued is on its way
-            arrived<EARLY + (J == 0 ? 2 : 0)>();
-#pragma unroll
-            for (int k = 0; k < STEPS; ++k) {
-#pragma unroll
-                for (int i = k * NEXT; i < (k + 1) * NEXT; ++i) {
-                    if (i == 0) read_we(b + 1, J + 1);
-                    if (i < T) read_w(J + 1, i);
-                    if (i >= T && i < 3 * T / 2) {
-                        read_x(J + 1, i - T);
-                        read_xe(b + 1, i - T);
-                    }
-                }
-                load_step(b + 2, J, STEPS + k);
-                product(J, k % T, T / 2 + k / T);
-                __builtin_amdgcn_sched_barrier(0);
-            }
-        };
         // An odd number of blocks is made even: codes past the last one are 0, and their scales padding.
-        for (int b = kb0; b < kb1; b += 2) {
-            block(b, std::integral_constant<int, 0>{});
-            block(b + 1, std::integral_constant<int, 1>{});
-        }
-        arrived<0>();                                        // nothing is on its way to LDS when the workgroup ends
-        asm volatile("s_nop 15\n\ts_nop 15");                // and the last sums are written
-    }
-
-    // A lane holds, of row wm + 16 m + lane % 16, columns 4 (lane / 16) + 0..3 of each 16; two exchanges of lanes
-    // give it eight neighbouring columns of each 32.
-#pragma unroll
-    for (int m = 0; m < T; ++m) {
-        const int64_t r = m0 + wm + 16 * m + row;
-#pragma unroll
-        for (int n = 0; n < T; n += 2) {
-            floatx8 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[n][m][i]), __float_as_uint(acc[n + 1][m][i]),
-                                                                false, false);
-                const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-                v[i] = __uint_as_float(y[0]);
-                v[4 + i] = __uint_as_float(y[1]);
+        const int kb1 = src.kb1;
+        for (int b0 = src.kb0; b0 < kb1; b0 += 2) {
+            const bool last = b0 + 2 >= kb1;
+            const bool group = last || (b0 & 2);             // the next pair's scales are in the other slot
+            int ahead = b0 + 2, scales_ahead = (b0 & ~3) + 4;
+            if (MANY && last) {                              // the blocks after these are the next tile's
+                src = source(number + gridDim.x);
+                ahead = scales_ahead = src.kb0;
             }
-            const int64_t col = n0 + wn + 16 * n + 8 * (lane >> 4);
-            if (r >= a.rows || col >= a.n) continue;
-            const int k = (int)min((int64_t)8, a.n - col);
-            if (parts)
-                store8_n(parts + ((int64_t)split * a.rows + r) * a.n + col, Vec8<float>::put(v), k);
-            else
-                put8((O*)a.y + r * a.ldy, col, a.n, v, k, a.accumulate != 0);
+            const int after = group ? slot ^ 1 : slot;
+            const auto load_step = [&](int stage, int k) {
+#pragma unroll
+                for (int j = 0; j < S::LOADS; ++j)
+                    if (FREE + j * SPREAD / S::LOADS == k) load(ahead + stage, stage, j);
+            };
+            // Block b0 + J, in stage J.  Beside the first one the scales of the next four blocks are loaded (twice, as
+            // that takes no branch: over one the compiler moves products past the barriers that they are to cover).
+            const auto block = [&](auto j) {
+                constexpr int J = decltype(j)::value;
+                const int sh = 8 * ((b0 & 2) + J);
+                we = ww[J] >> sh;
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k) {
+                    if (k < T / 2) {
+                        read_x(J, T / 2 + k);
+                        read_xe(slot, T / 2 + k);
+                    }
+                    if (k == FREE) {
+                        all_read();
+                        if (J == 0) load_scales(scales_ahead, slot ^ 1);
+                    }
+                    load_step(J, k);
+                    product(J, k % T, k / T, sh);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                // the next block is whole in LDS; only what has just been issued, and a tile's stores, are on their way
+                if (J == 0 && MANY) {
+                    if (!storing) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(EARLY + 2) : "memory");
+                    storing = false;
+                }
+                arrived<EARLY + (J == 0 ? 2 + STORES : 0)>();
+                const int then = J == 0 ? slot : after;
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k) {
+#pragma unroll
+                    for (int i = k * NEXT; i < (k + 1) * NEXT; ++i) {
+                        if (i == 0) read_we(then, J + 1);
+                        if (i < T) read_w(J + 1, i);
+                        if (i >= T && i < 3 * T / 2) {
+                            read_x(J + 1, i - T);
+                            read_xe(then, i - T);
+                        }
+                    }
+                    load_step(J, STEPS + k);
+                    product(J, k % T, T / 2 + k / T, sh);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            block(std::integral_constant<int, 0>{});
+            block(std::integral_constant<int, 1>{});
+            if (group) slot ^= 1;
         }
+        asm volatile("s_nop 15\n\ts_nop 15");                // the last sums are written
+
+        // A lane holds, of row wm + 16 m + lane % 16, columns 4 (lane / 16) + 0..3 of each 16; two exchanges of lanes
+        // give it eight neighbouring columns of each 32.
+        int split, tile_m, tile_n;
+        place(plan, number, split, tile_m, tile_n);
+        const int64_t m0 = (int64_t)tile_m * S::SIDE, n0 = (int64_t)tile_n * S::SIDE;
+        int here = lane;
+        asm volatile("" : "+v"(here));                       // the places of outputs are not kept beside the products
+#pragma unroll
+        for (int m = 0; m < T; ++m) {
+            const int64_t r = m0 + wm + 16 * m + (here & 15);
+#pragma unroll
+            for (int n = 0; n < T; n += 2) {
+                __builtin_amdgcn_sched_barrier(0);
+                floatx8 v;
+                floatx4 lo = acc[n][m], hi = acc[n + 1][m];
+                if constexpr (!EXACT)
+                    // Read here: the compiler would read all of them before the first store, into registers that it does
+                    // not have.  An exchange of lanes needs two states behind the instruction that wrote its operands.
+                    asm volatile("v_accvgpr_read_b32 %0, %8\n\tv_accvgpr_read_b32 %1, %9\n\t"
+                                 "v_accvgpr_read_b32 %2, %10\n\tv_accvgpr_read_b32 %3, %11\n\t"
+                                 "v_accvgpr_read_b32 %4, %12\n\tv_accvgpr_read_b32 %5, %13\n\t"
+                                 "v_accvgpr_read_b32 %6, %14\n\tv_accvgpr_read_b32 %7, %15\n\ts_nop 1"
+                                 : "=v"(lo[0]), "=v"(lo[1]), "=v"(lo[2]), "=v"(lo[3]), "=v"(hi[0]), "=v"(hi[1]),
+                                   "=v"(hi[2]), "=v"(hi[3])
+                                 : "a"(acc[n][m][0]), "a"(acc[n][m][1]), "a"(acc[n][m][2]), "a"(acc[n][m][3]),
+                                   "a"(acc[n + 1][m][0]), "a"(acc[n + 1][m][1]), "a"(acc[n + 1][m][2]), "a"(acc[n + 1][m][3]));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo[i]), __float_as_uint(hi[i]), false, false);
+                    const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+                    v[i] = __uint_as_float(y[0]);
+                    v[4 + i] = __uint_as_float(y[1]);
+                }
+                const int64_t col = n0 + wn + 16 * n + 8 * (here >> 4);
+                if (r >= a.rows || col >= a.n) continue;
+                const int k = (int)min((int64_t)8, a.n - col);
+                if (parts)
+                    store8_n(parts + ((int64_t)split * a.rows + r) * a.n + col, Vec8<float>::put(v), k);
+                else
+                    put8((O*)a.y + r * a.ldy, col, a.n, v, k, a.accumulate != 0);
+            }
+        }
+        number += gridDim.x;
+        if (!MANY || number >= all) break;
+        // fewer stores than arrived() counts on: nothing is left on its way
+        storing = m0 + wm + 16 * T <= a.rows && n0 + wn + 16 * T <= a.n;
+        if (!storing) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int n = 0; n < T; ++n)
+#pragma unroll
+            for (int m = 0; m < T; ++m) acc[n][m] = floatx4{};
     }
+    arrived<0>();                                            // nothing is on its way to LDS when the workgroup ends
 }
 
 // Y (+)= the ranges' sums, in order; V consecutive elements of a row a thread.
@@ -514,7 +577,8 @@ hipError_t launch_tiles(const Linear& a, const TilePlan& p, float* parts, hipStr
     static const hipError_t attr = hipFuncSetAttribute((const void*)linear_tile_kernel<EXACT, T, O>,
                                                        hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS_BYTES);
     if (attr != hipSuccess) return attr;
-    S4_LAUNCH((linear_tile_kernel<EXACT, T, O>), dim3((uint32_t)(p.tiles_m * p.tiles_n * p.splits)), dim3(256),
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
+    S4_LAUNCH((linear_tile_kernel<EXACT, T, O>), dim3((uint32_t)(T == 8 ? std::min<int64_t>(tiles, 256) : tiles)), dim3(256),
               S::LDS_BYTES, stream, a, p, p.splits > 1 ? parts : nullptr);
     if (p.splits > 1) {
         const bool four = a.n % 4 == 0;

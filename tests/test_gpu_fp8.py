@@ -251,6 +251,35 @@ def test_linear_not_finite_on_the_largest_tiles():
     assert torch.equal(torch.isnan(y), bad) and torch.equal(y[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("t,n,k", [(16384, 4096, 256), (16130, 4090, 300), (12289, 5000, 1160), (16384, 4096, 700)])
+def test_linear_many_large_tiles(t, n, k):
+    """More tiles than CUs, one after the other in a workgroup: what rows give does not depend on how many are with
+    them, to the last bit, and the oracle holds on some of them.  Edges, odd numbers of blocks, added, odd strides."""
+    require_gpu()
+    from bit_quantized_shampoo_amd import fp8_linear, fp8_load, fp8_store, fp8_store_weight
+    g = torch.Generator(device="cuda").manual_seed(t + k)
+    x = torch.randn(t, k, generator=g, device="cuda").bfloat16()
+    w8 = fp8_store_weight(torch.randn(n, k, generator=g, device="cuda"))
+    announce(f"fp8 linear of many large tiles {t}x{n}x{k}")
+    y = fp8_linear(x, w8)
+    for i in range(0, t, 1000):
+        assert torch.equal(y[i:i + 1000], fp8_linear(x[i:i + 1000].contiguous(), w8)), i
+    wd = fp8_load(w8, dtype=torch.float32).double().cpu()
+    for i in (0, 255, 256, 8191, t - 1):
+        xd = fp8_load(fp8_store(x[i:i + 1]), dtype=torch.float32).double().cpu()
+        ref, size = (xd @ wd.T)[0], (xd.abs() @ wd.abs().T)[0]
+        assert bool(((y[i].double().cpu() - ref).abs() <= 7 * 2.0 ** -13 * size + 2.0 ** -8 * ref.abs() + 1e-30).all()), i
+    for ld in (n + 8, n + 1):
+        out = torch.full((t, ld), 0.5, dtype=torch.bfloat16, device="cuda")
+        for _ in range(2):
+            fp8_linear(x, w8, out=out[:, :n], accumulate=True)
+        want = torch.full((t, n), 0.5, dtype=torch.bfloat16, device="cuda")
+        for i in range(0, t, 1000):
+            for _ in range(2):
+                fp8_linear(x[i:i + 1000].contiguous(), w8, out=want[i:i + 1000], accumulate=True)
+        assert torch.equal(out[:, :n], want) and bool((out[:, n:] == 0.5).all())
+
+
 def test_linear_does_not_depend_on_other_rows():
     """Rows behind the last and columns behind the last weight row are neither read nor written."""
     require_gpu()
