@@ -208,11 +208,11 @@ __device__ __forceinline__ bf16x8 widen(u32x4 c, int q) {
 // Four waves, 2 x 2, each with T x T blocks of 16 x 16 outputs; two stages of a block of k.
 //
 // With T = 8 a wave's 128 x 128 outputs take 256 registers of sums, and a wave reads 32 KB of LDS for the 64
-// instructions of a block of k: the matrix cores are what is busy.  16384 x 4096 x 4096 takes 224-253 us (2.2-2.45
-// PFLOP/s; a library's fp8 product with one scale for a whole tensor 203-230).  A block of k takes 1.25 us,
-// where the instructions alone take 0.85 at the full clock: on random codes the card holds its power, not its
-// clock (on zeros a block takes 1.0).  The rest is a tile's first loads and its stores.  The instruction of 32 x 32 x 64
-// reaches 3.93 PFLOP/s by itself where this one has 4.28.  Exact products: 160 us for 4096 x 4096 x 4096 (55-60).
+// instructions of a block of k: the matrix cores are what is busy.  8192 x 8192 x 8192 takes 396 us (2.77 PFLOP/s; a
+// library's fp8 product with one scale for a whole tensor 350), 16384 x 4096 x 4096 243 (2.26; 227), 4096 x 4096 x 4096
+// 55 (2.49; 48.5).  On random codes the card holds its power, not its clock (1.8 GHz at the second size; a block of k takes
+// 1.0 us on zeros); beside that stand the outputs, 134 MB in bursts of a tile a CU.  The instruction of 32 x 32 x 64
+// reaches 3.93 PFLOP/s by itself where this one has 4.28.  Exact products take 164 us for 4096 x 4096 x 4096.
 template <int T>
 struct TileShape {
     static constexpr int SIDE = 32 * T;                      // rows of X, and of W
@@ -438,45 +438,75 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(Linear a, TilePlan pla
         const int64_t m0 = (int64_t)tile_m * S::SIDE, n0 = (int64_t)tile_n * S::SIDE;
         int here = lane;
         asm volatile("" : "+v"(here));                       // the places of outputs are not kept beside the products
+        const auto sums = [&](int n, int m) {                // of columns 16 n .. 16 n + 31
+            __builtin_amdgcn_sched_barrier(0);
+            floatx4 lo = acc[n][m], hi = acc[n + 1][m];
+            if constexpr (!EXACT)
+                // Read here: the compiler would read all of them before the first store, into registers that it does
+                // not have.  An exchange of lanes needs two states behind the instruction that wrote its operands.
+                asm volatile("v_accvgpr_read_b32 %0, %8\n\tv_accvgpr_read_b32 %1, %9\n\t"
+                             "v_accvgpr_read_b32 %2, %10\n\tv_accvgpr_read_b32 %3, %11\n\t"
+                             "v_accvgpr_read_b32 %4, %12\n\tv_accvgpr_read_b32 %5, %13\n\t"
+                             "v_accvgpr_read_b32 %6, %14\n\tv_accvgpr_read_b32 %7, %15\n\ts_nop 1"
+                             : "=v"(lo[0]), "=v"(lo[1]), "=v"(lo[2]), "=v"(lo[3]), "=v"(hi[0]), "=v"(hi[1]),
+                               "=v"(hi[2]), "=v"(hi[3])
+                             : "a"(acc[n][m][0]), "a"(acc[n][m][1]), "a"(acc[n][m][2]), "a"(acc[n][m][3]),
+                               "a"(acc[n + 1][m][0]), "a"(acc[n + 1][m][1]), "a"(acc[n + 1][m][2]), "a"(acc[n + 1][m][3]));
+            floatx8 v;
 #pragma unroll
-        for (int m = 0; m < T; ++m) {
-            const int64_t r = m0 + wm + 16 * m + (here & 15);
-#pragma unroll
-            for (int n = 0; n < T; n += 2) {
-                __builtin_amdgcn_sched_barrier(0);
-                floatx8 v;
-                floatx4 lo = acc[n][m], hi = acc[n + 1][m];
-                if constexpr (!EXACT)
-                    // Read here: the compiler would read all of them before the first store, into registers that it does
-                    // not have.  An exchange of lanes needs two states behind the instruction that wrote its operands.
-                    asm volatile("v_accvgpr_read_b32 %0, %8\n\tv_accvgpr_read_b32 %1, %9\n\t"
-                                 "v_accvgpr_read_b32 %2, %10\n\tv_accvgpr_read_b32 %3, %11\n\t"
-                                 "v_accvgpr_read_b32 %4, %12\n\tv_accvgpr_read_b32 %5, %13\n\t"
-                                 "v_accvgpr_read_b32 %6, %14\n\tv_accvgpr_read_b32 %7, %15\n\ts_nop 1"
-                                 : "=v"(lo[0]), "=v"(lo[1]), "=v"(lo[2]), "=v"(lo[3]), "=v"(hi[0]), "=v"(hi[1]),
-                                   "=v"(hi[2]), "=v"(hi[3])
-                                 : "a"(acc[n][m][0]), "a"(acc[n][m][1]), "a"(acc[n][m][2]), "a"(acc[n][m][3]),
-                                   "a"(acc[n + 1][m][0]), "a"(acc[n + 1][m][1]), "a"(acc[n + 1][m][2]), "a"(acc[n + 1][m][3]));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo[i]), __float_as_uint(hi[i]), false, false);
-                    const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-                    v[i] = __uint_as_float(y[0]);
-                    v[4 + i] = __uint_as_float(y[1]);
-                }
-                const int64_t col = n0 + wn + 16 * n + 8 * (here >> 4);
-                if (r >= a.rows || col >= a.n) continue;
-                const int k = (int)min((int64_t)8, a.n - col);
-                if (parts)
-                    store8_n(parts + ((int64_t)split * a.rows + r) * a.n + col, Vec8<float>::put(v), k);
-                else
-                    put8((O*)a.y + r * a.ldy, col, a.n, v, k, a.accumulate != 0);
+            for (int i = 0; i < 4; ++i) {
+                const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(lo[i]), __float_as_uint(hi[i]), false, false);
+                const auto y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+                v[i] = __uint_as_float(y[0]);
+                v[4 + i] = __uint_as_float(y[1]);
             }
+            return v;
+        };
+        // Whole tiles apart: the code for edges is there for every m and n, more of it than the instruction cache holds
+        // (16384 x 4096 x 1024 takes 72 us, and 81 where all tiles go that way).
+        const bool whole = m0 + wm + 16 * T <= a.rows && n0 + wn + 16 * T <= a.n;
+        const int64_t r0 = m0 + wm + (here & 15), c0 = n0 + wn + 8 * (here >> 4);
+        if (whole && parts) {
+            float* p = parts + ((int64_t)split * a.rows + r0) * a.n + c0;
+#pragma unroll
+            for (int m = 0; m < T; ++m, p += 16 * a.n)
+#pragma unroll
+                for (int n = 0; n < T; n += 2) store8(p + 16 * n, Vec8<float>::put(sums(n, m)));
+        } else if (whole && a.accumulate) {
+            O* p = (O*)a.y + r0 * a.ldy + c0;
+#pragma unroll
+            for (int m = 0; m < T; ++m, p += 16 * a.ldy) {
+                typename Vec8<O>::Raw y[T / 2];
+#pragma unroll
+                for (int n = 0; n < T; n += 2) y[n / 2] = load8(p + 16 * n);
+#pragma unroll
+                for (int n = 0; n < T; n += 2) store8(p + 16 * n, Vec8<O>::put(Vec8<O>::get(y[n / 2]) + sums(n, m)));
+            }
+        } else if (whole) {
+            O* p = (O*)a.y + r0 * a.ldy + c0;
+#pragma unroll
+            for (int m = 0; m < T; ++m, p += 16 * a.ldy)
+#pragma unroll
+                for (int n = 0; n < T; n += 2) store8(p + 16 * n, Vec8<O>::put(sums(n, m)));
+        } else {
+#pragma unroll
+            for (int m = 0; m < T; ++m)
+#pragma unroll
+                for (int n = 0; n < T; n += 2) {
+                    const floatx8 v = sums(n, m);
+                    const int64_t r = r0 + 16 * m, col = c0 + 16 * n;
+                    if (r >= a.rows || col >= a.n) continue;
+                    const int k = (int)min((int64_t)8, a.n - col);
+                    if (parts)
+                        store8_n(parts + ((int64_t)split * a.rows + r) * a.n + col, Vec8<float>::put(v), k);
+                    else
+                        put8((O*)a.y + r * a.ldy, col, a.n, v, k, a.accumulate != 0);
+                }
         }
         number += gridDim.x;
         if (!MANY || number >= all) break;
         // fewer stores than arrived() counts on: nothing is left on its way
-        storing = m0 + wm + 16 * T <= a.rows && n0 + wn + 16 * T <= a.n;
+        storing = whole;
         if (!storing) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int n = 0; n < T; ++n)
