@@ -618,7 +618,7 @@ def fp8_linear(x, w8: Fp8, out: torch.Tensor | None = None, accumulate: bool = F
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """x w8^T, [x rows, w8 rows].  x is an Fp8 of fp8_store (or block_norm_forward), or a matrix, which the
     call quantises in the same way.  The result is of `dtype` (default: x's type, bfloat16 for an Fp8),
-    or goes into `out`, of its own type; accumulate=True adds to `out`.
+    or goes into `out`, of its own type; accumulate=True adds to `out`, which shares no memory with x or w8.
 
     A bfloat16 result's products are the 8-bit matrix cores', which cut a term off 13 bits below the largest
     of its eight neighbours (at most a quarter of bfloat16's rounding); those of a float32 or float16
@@ -649,6 +649,8 @@ def fp8_linear(x, w8: Fp8, out: torch.Tensor | None = None, accumulate: bool = F
     else:
         ldo = _matrix(out, "out", dtype, rows, n, dev)
         odt = out.dtype
+        if rows and out.data_ptr() == (xp or xc):
+            raise ValueError("out must not be x")
     lib = L.lib()
     o = _DTYPES[odt]
     ws, wp, wb = _workspace(workspace, lib.shampoo4_fp8_linear_workspace_bytes(o, rows, n, k, not xp), held)

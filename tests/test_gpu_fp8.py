@@ -280,6 +280,18 @@ def test_linear_many_large_tiles(t, n, k):
         assert torch.equal(out[:, :n], want) and bool((out[:, n:] == 0.5).all())
 
 
+def test_linear_into_its_input_is_refused():
+    require_gpu()
+    from bit_quantized_shampoo_amd import fp8_linear, fp8_store_weight
+    x = torch.randn(5, 64, device="cuda").bfloat16()
+    w8 = fp8_store_weight(torch.randn(64, 64, device="cuda"))
+    announce("fp8 linear into its input")
+    with pytest.raises(ValueError):
+        fp8_linear(x, w8, out=x)
+    with pytest.raises(ValueError):
+        fp8_linear(x, w8, out=x, accumulate=True)
+
+
 def test_linear_does_not_depend_on_other_rows():
     """Rows behind the last and columns behind the last weight row are neither read nor written."""
     require_gpu()
