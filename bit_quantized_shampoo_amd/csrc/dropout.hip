@@ -1,7 +1,8 @@
 // Dropout of a matrix with a mask that is never stored (random.hpp).
 //
 // A stream: a lane takes eight columns of ROWS rows, all loads in flight before the generator's
-// first use.
+// first use.  Bytes bound it: 16384 x 4096 bf16 takes 43-50 us (268 MB), the generator's 40 instructions for
+// eight elements beside them.
 #include "random.hpp"
 #include "train.hpp"
 
