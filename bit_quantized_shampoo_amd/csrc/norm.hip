@@ -277,8 +277,9 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
 }
 
 // A whole pass (WHOLE), or, for rows of more than BLOCK_WIDE columns, two: the rows' two sums (SUMS), and the rest by
-// ranges of columns, with those sums given (REST).  Registers hold a row of 8192 columns with its sums over rows, 16
-// vectors' worth a lane; one more is spilled, and 4096 x 16384 bf16 in one pass took 2940 us, in two 290-296.
+// ranges of columns, with those sums given (REST): 10 values an element move instead of 6.  Registers hold two
+// vectors a lane beside the factors and sums over rows that belong to them; three were spilled, and
+// 4096 x 16384 bf16 in one pass took 2940 us, in two 290-296.
 enum Pass { WHOLE, SUMS, REST };
 template <class T, int WPR, int VPT, bool DROP, bool TOKEN, Pass PASS = WHOLE>
 __global__ __launch_bounds__(threads_of(WPR), 2) void block_backward_kernel(BlockBackward a, Drop d) {
