@@ -269,7 +269,8 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
         if (a.y) c.template store_raw<T>((T*)a.y + row * a.ldy, i, y);
         if (a.yc) {
             const floatx8 f = Vec8<T>::get(y);
-            const uint32_t e = fp8_exponent(max16(magnitude(f)));
+            // past the row's end a factor that is NaN has made NaN of zeros, which are no part of a block
+            const uint32_t e = fp8_exponent(max16(c.at(i) < cols ? magnitude(f) : 0u));
             if (c.at(i) < pitch) stg((u32x2*)(a.yc + row * pitch + c.at(i)), Fp8Block(e).codes(f));
             if ((t & 15) == 0 && c.at(i) >> 7 < sp) stg(a.ys + row * sp + (c.at(i) >> 7), (uint8_t)e);
         }
