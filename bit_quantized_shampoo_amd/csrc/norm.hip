@@ -123,6 +123,12 @@ struct Cols {
     __device__ __forceinline__ void store(T* row, int i, floatx8 v) const {
         store_raw(row, i, Vec8<T>::put(v));
     }
+    // Zeros past the row's end.
+    __device__ __forceinline__ floatx8 own(floatx8 v, int i) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = at(i) + j < cols ? v[j] : 0.f;
+        return v;
+    }
     // Eight values of a vector that every row shares, and how they are finished; ones where there is no
     // vector.
     __device__ __forceinline__ u32x8 shared(const float* p, int i) const {
@@ -243,7 +249,12 @@ __global__ __launch_bounds__(threads_of(WPR)) void block_forward_kernel(BlockFor
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             floatx8 z = Vec8<T>::get(h[i]) * (DROP ? hr * d.scale : hr) * c.finish_shared(a.post, rp[i], i);
-            if (DROP) z = drop8(z, keep[i], d);
+            if (DROP) {
+                z = drop8(z, keep[i], d);
+                // A norm that is NaN makes it of the zeros past the row's end too.  Where all of the row's own are dropped
+                // those must not reach its sum of squares (else the row is NaN by what is its own).
+                if (hr != hr) z = c.own(z, i);
+            }
             if (TOKEN)
                 z *= Vec8<T>::get(g[i]);
             else
