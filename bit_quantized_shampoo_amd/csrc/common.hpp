@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace s4 {
 
 // Optional start/stop events for the next kernel launch.  A timed launch goes through
@@ -27,6 +29,25 @@ inline LaunchTiming& launch_timing() {
             hipLaunchKernelGGL(kernel, grid, block, shmem, stream, __VA_ARGS__);                  \
         lt_.start = lt_.stop = nullptr;                                                           \
     } while (0)
+
+// A kernel's limit of dynamic LDS (64 KB until it is raised), one object for each kernel.  The runtime keeps it for
+// the device that is current when it is set, so every device has it raised before its first launch there, and again
+// after a failure.  Calls at the same time may both raise it, to the same value.
+class LdsLimit {
+    std::atomic<uint64_t> raised_{0};                        // a bit for each of the first 64 devices
+
+public:
+    hipError_t raise(const void* kernel, size_t bytes) {
+        int device = 0;
+        hipError_t e = hipGetDevice(&device);
+        if (e != hipSuccess) return e;
+        const uint64_t bit = device < 64 ? uint64_t(1) << device : 0;
+        if (raised_.load(std::memory_order_acquire) & bit) return hipSuccess;
+        e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == hipSuccess) raised_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));

@@ -604,9 +604,9 @@ hipError_t launch_rows(const Linear& a, hipStream_t stream) {
 template <bool EXACT, int T, class O>
 hipError_t launch_tiles(const Linear& a, const TilePlan& p, float* parts, hipStream_t stream) {
     using S = TileShape<T>;
-    static const hipError_t attr = hipFuncSetAttribute((const void*)linear_tile_kernel<EXACT, T, O>,
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS_BYTES);
-    if (attr != hipSuccess) return attr;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void*)linear_tile_kernel<EXACT, T, O>, S::LDS_BYTES);
+    if (e != hipSuccess) return e;
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     S4_LAUNCH((linear_tile_kernel<EXACT, T, O>), dim3((uint32_t)(T == 8 ? std::min<int64_t>(tiles, 256) : tiles)), dim3(256),
               S::LDS_BYTES, stream, a, p, p.splits > 1 ? parts : nullptr);

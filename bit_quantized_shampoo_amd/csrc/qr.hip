@@ -1173,11 +1173,11 @@ __global__ __launch_bounds__(PANEL_THREADS) void panel_global_kernel(const Panel
 
 template <int NR>
 hipError_t launch_reg(const PanelDesc* descs, int ndesc, int max_h, hipStream_t stream) {
-    // the dynamic-LDS limit is raised once per instantiation (to the largest panel it serves)
-    static const hipError_t attr = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&panel_reg_kernel<NR>), hipFuncAttributeMaxDynamicSharedMemorySize,
-        (int)panel_lds_bytes(true, NSLOT * NR < PANEL_LDS_MAX_ROWS ? NSLOT * NR : PANEL_LDS_MAX_ROWS));
-    if (attr != hipSuccess) return attr;
+    // the dynamic-LDS limit of an instantiation is raised to the largest panel it serves
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(&panel_reg_kernel<NR>),
+                                     panel_lds_bytes(true, NSLOT * NR < PANEL_LDS_MAX_ROWS ? NSLOT * NR : PANEL_LDS_MAX_ROWS));
+    if (e != hipSuccess) return e;
     const size_t lds = panel_lds_bytes(true, max_h);
     S4_LAUNCH(panel_reg_kernel<NR>, dim3(ndesc), dim3(PANEL_THREADS), lds, stream, descs);
     return hipGetLastError();
@@ -1186,10 +1186,10 @@ hipError_t launch_reg(const PanelDesc* descs, int ndesc, int max_h, hipStream_t 
 template <int NR>
 hipError_t launch_step(const StepPanelDesc* panels, int npanel, const SlabDesc* slabs, int nslab, int max_h,
                        hipStream_t stream) {
-    static const hipError_t attr = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(&qr_step_kernel<NR>), hipFuncAttributeMaxDynamicSharedMemorySize,
-        (int)qr_step_lds_bytes(NSLOT * NR < PANEL_LDS_MAX_ROWS ? NSLOT * NR : PANEL_LDS_MAX_ROWS));
-    if (attr != hipSuccess) return attr;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise(reinterpret_cast<const void*>(&qr_step_kernel<NR>),
+                                     qr_step_lds_bytes(NSLOT * NR < PANEL_LDS_MAX_ROWS ? NSLOT * NR : PANEL_LDS_MAX_ROWS));
+    if (e != hipSuccess) return e;
     S4_LAUNCH(qr_step_kernel<NR>, dim3(npanel + nslab), dim3(PANEL_THREADS), qr_step_lds_bytes(max_h), stream,
               panels, npanel, slabs);
     return hipGetLastError();

@@ -408,9 +408,9 @@ WPlan wgrad_plan(int64_t rows, int64_t n, int64_t cols, int pieces) {
 template <class T, int WM, int WN, int TM, int TN, int KS>
 hipError_t wgrad_launch(const WGrad& w, const WPlan& p, hipStream_t stream) {
     using S = Shape<T, WM, WN, TM, TN, KS>;
-    static const hipError_t attr = hipFuncSetAttribute((const void*)wgrad_kernel<T, WM, WN, TM, TN, KS>,
-                                                       hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::LDS_BYTES);
-    if (attr != hipSuccess) return attr;
+    static LdsLimit limit;
+    const hipError_t e = limit.raise((const void*)wgrad_kernel<T, WM, WN, TM, TN, KS>, S::LDS_BYTES);
+    if (e != hipSuccess) return e;
     S4_LAUNCH((wgrad_kernel<T, WM, WN, TM, TN, KS>), dim3((uint32_t)(p.tiles_m * p.tiles_n * p.splits)),
               dim3(S::THREADS), S::LDS_BYTES, stream, w, (int)p.tiles_m, (int)p.tiles_n, p.rows_per, p.splits > 1);
     return hipSuccess;
