@@ -220,11 +220,13 @@ __device__ __forceinline__ bf16x8 widen(u32x4 c, int q) {
 // Four waves, 2 x 2, each with T x T blocks of 16 x 16 outputs; two stages of a block of k.
 //
 // With T = 8 a wave's 128 x 128 outputs take 256 registers of sums, and a wave reads 32 KB of LDS for the 64
-// instructions of a block of k: the matrix cores are what is busy.  8192 x 8192 x 8192 takes 396 us (2.77 PFLOP/s; a
-// library's fp8 product with one scale for a whole tensor 350), 16384 x 4096 x 4096 243 (2.26; 227), 4096 x 4096 x 4096
-// 55 (2.49; 48.5).  On random codes the card holds its power, not its clock (1.8 GHz at the second size; a block of k takes
-// 1.0 us on zeros); beside that stand the outputs, 134 MB in bursts of a tile a CU.  The instruction of 32 x 32 x 64
-// reaches 3.93 PFLOP/s by itself where this one has 4.28.  Exact products take 164 us for 4096 x 4096 x 4096.
+// instructions of a block of k: the matrix cores are what is busy.  Behind hundreds of launches, with the card settled,
+// 8192 x 8192 x 8192 takes 391 us (2.81 PFLOP/s; a library's fp8 product with one scale for a whole tensor 343),
+// 16384 x 4096 x 4096 212 (2.59; 185), 4096 x 4096 x 4096 55 (2.48; 49).  On random codes the card holds its power, not its
+// clock: after a pause the second size takes 240-247 us over the first 60 launches (the library 222), between 212 and
+// 299 each, and 174 on zeros.  Beside that stand the outputs, 134 MB in bursts of a tile a CU.  The instruction of
+// 32 x 32 x 64 reaches 3.93 PFLOP/s by itself where this one has 4.28.  Exact products take 157 us for
+// 4096 x 4096 x 4096.
 template <int T>
 struct TileShape {
     static constexpr int SIDE = 32 * T;                      // rows of X, and of W
@@ -556,16 +558,25 @@ struct LinearPlan {
     TilePlan plan;
 };
 
-// Few rows read W as it lies, and quantise X within the product; beyond 16 rows that is worth it while the
-// workgroups that do it again are few and k is short (64 x 4096 x 1024 takes 6.0 us by rows and
-// 5.8 on tiles after 3.9 for quantising).
+// Few rows read W as it lies, and quantise X within the product; beyond 16 rows that is done while the
+// workgroups that do it again are few and k is short.  Both sides, in us of a call of a captured graph on a bf16 X, by
+// rows / on tiles behind the quantising: for n x k of
+//               1024 x 1024  4096 x 1024  8192 x 1024  4096 x 2048  8192 x 2048  4096 x 4096  14336 x 4096
+//   16 rows     4.2 / 8.6    4.4 / 8.7    5.9 / 8.6    8.9 / 11     17 / 11      9.9 / 12     34 / 20
+//   32          5.8 / 9.0    6.1 / 9.0    8.6 / 8.9    9.2 / 12     17 / 12      14 / 13      49 / 20
+//   64          9.1 / 9.2    9.3 / 9.1    18 / 9.1     14 / 12      25 / 12      24 / 14      82 / 20
+// The cut-offs are wider than that: by rows is the slower side from 8192 x 2048 on, and with more than 32 rows from
+// 2^23 elements of W on.
 //
 // Tiles and ranges of k by an estimate of the time, of what was measured: with c workgroups a CU, a block of
 // k takes 0.2 c us on 64 x 64 tiles (0.23 at least), 0.1 + 0.46 c on 128 x 128 and 1.3 c on 256 x 256;
 // with exact products 0.3 + 0.33 c and 1.26 c (1.45 at least).  Beside that a launch takes 4 us (8 on
-// the largest tiles), and joining ranges 3 us and their bytes.  1024 x 4096 x 4096 bf16 takes 29.7,
-// 23.4 and 47 us on the three tiles, 777 x 577 x 1153 7.3, 10.5 and 28, 4096 x 4096 x 1024 33, 27 and
-// 23.5, 8192 x 1024 x 4096 53, 33 and 50; 300 x 300 x 4096 fp32 22 us in one range and 12 in four.
+// the largest tiles), and joining ranges 3 us and their bytes.  The outputs' bytes are left out, as every tile writes the
+// same: 16384 x 4096 x 1024 takes 127, 89 and 73 us on the three tiles, 21, 25 and 24 above the estimate.  At 28 sizes
+// measured on every tile and number of ranges the choice is the fastest or within 7% of it (1024 x 1024 x 8192 fp32 39.6 us
+// in four ranges on 128 x 128, 37.0 on 64 x 64).  1024 x 4096 x 4096 bf16 takes 31, 24 and 47 us on the three
+// tiles, 777 x 577 x 1153 6.8, 11 and 29, 4096 x 4096 x 1024 37, 28 and 24, 8192 x 1024 x 4096 55, 35 and 52;
+// 300 x 300 x 4096 fp32 23 us in one range and 12 in four.
 LinearPlan linear_plan(bool exact, int64_t rows, int64_t n, int64_t k) {
     LinearPlan best{};
     const int64_t pitch = fp8_pitch(k);

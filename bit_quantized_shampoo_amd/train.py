@@ -728,7 +728,8 @@ def block_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, h: t
     Returns (x', y, y8, stats): y8 is y quantised as by fp8_store (None without save8), stats is what
     block_norm_backward needs.  Without `h`, x' is x (the norm alone); without `weight` there is no y;
     without `post_weight` the block's end is h as it is.  gate: float32 [cols], a matrix like x, or None
-    for 1.  Weights are float32 [cols].  p, seed, offset, counter: as of dropout.  `out` may be x or h."""
+    for 1.  Weights are float32 [cols].  p, seed, offset, counter: as of dropout (which h is needed for).
+    `out` may be x or h, and `y` may be h."""
     ldx = _matrix(x, "x")
     rows, cols = x.shape
     dev, dtype = x.device, x.dtype

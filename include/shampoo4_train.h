@@ -295,6 +295,8 @@ SHAMPOO4_API shampoo4_status shampoo4_dropout(const shampoo4_dropout_config* cfg
  * y_codes and y_scales (both or none) receive y as rounded, quantised as by shampoo4_fp8_store:
  * the next product's operand.  With h NULL, residual_scale must be 1, and post_weight, gate, out
  * and h_rstd NULL.  out may be x or h itself, and y may be h, each with its leading dimension.
+ * With h NULL nothing is dropped.  A gate that is not finite makes NaN where it is dropped too, in x' (0 gate) and
+ * in the backward pass, where what is dropped is g.
  * eps: at least 1e-30, finite.  Finite rows of any size have their norm (squares beyond fp32 are taken
  * of the row divided by a power of two).
  * ESHAPE: cols above 16384, or 2^24 rows or more (2^23 from 2049 columns on, 2^22 from 4097 on). */
@@ -317,7 +319,7 @@ SHAMPOO4_API shampoo4_status shampoo4_block_norm_forward(const shampoo4_block_no
  *     xh = x' rstd;  t = dy weight;  g = dres + rstd (t - xh mean(t xh))      (weight NULL: g = dres)
  *     dx = residual_scale g;  dweight = sum over rows of dy xh
  *     hh = h h_rstd;  z = drop(hh post_weight);  dgate = g z (gate_rows = 1), or its sum over rows
- *     d = drop(g gate);  dpost_weight = sum over rows of d hh;  u = d post_weight
+ *     d = gate drop(g);  dpost_weight = sum over rows of d hh;  u = d post_weight
  *     dh = h_rstd (u - hh mean(u hh))     (post_weight NULL: z = drop(h), dh = d)
  * dx, dh and a matrix dgate are of `dtype` and may be NULL; dweight, dpost_weight and a vector dgate
  * are fp32 [cols], written in whole (rows = 0: zeros), and may be NULL.  dx may be dres or dy itself,
