@@ -334,6 +334,7 @@ shampoo4_status shampoo4_fp8_store_weight(shampoo4_dtype dtype, int64_t rows, in
     S4_TRY(matrix_ok(w, dtype, rows, cols, ldw));
     S4_TRY(fp8_ok(codes, scales, rows));
     if (t_codes) S4_TRY(fp8_ok(t_codes, t_scales, rows));
+    if (rows > 0 && t_codes && (t_codes == codes || t_scales == scales)) return SHAMPOO4_EINVAL;
     return launched(launch_fp8_store_weight(dtype, rows, cols, w, ldw, codes, scales, t_codes, t_scales,
                                             as_stream(stream)));
 }
@@ -410,6 +411,7 @@ shampoo4_status shampoo4_block_norm_forward(const shampoo4_block_norm_config* cf
     if (y_codes) S4_TRY(fp8_ok(y_codes, y_scales, rows));
     if (!h && !weight) return SHAMPOO4_EINVAL;
     if (!aligned(weight, 4) || !aligned(post_weight, 4) || !aligned(rstd, 4) || !aligned(h_rstd, 4)) return SHAMPOO4_EALIGN;
+    if (out && out == y) return SHAMPOO4_EINVAL;             // one result over the other
     const BlockForward a{x, h, post_weight, gate, weight, out, y, y_codes, y_scales, h_rstd, rstd, rows, cols, ldx, ldh,
                          ldgate, ldout, ldy, cfg->eps, cfg->residual_scale, gate_rows};
     return launched(launch_block_forward(dtype, a, d, as_stream(stream)));
@@ -460,6 +462,8 @@ shampoo4_status shampoo4_block_norm_backward(const shampoo4_block_norm_config* c
         return SHAMPOO4_EALIGN;
     if (dweight || dpost_weight || (dgate && !gate_rows) || cols > BLOCK_WIDE)
         S4_TRY(workspace_ok(workspace, workspace_bytes, block_workspace_bytes(rows, cols)));
+    // one result over the other
+    if (rows > 0 && ((dx && dx == dh) || (dgate && gate_rows && (dgate == dx || dgate == dh)))) return SHAMPOO4_EINVAL;
     const BlockBackward a{dy, dres, x, h, gate, rstd, weight, h_rstd, post_weight, dx, dh, dgate, dweight, dpost_weight,
                           (float*)workspace, nullptr, rows, cols, lddy, lddres, ldx, ldh, ldgate, lddx, lddh, lddgate,
                           cfg->residual_scale, gate_rows};

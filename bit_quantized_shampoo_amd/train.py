@@ -571,7 +571,8 @@ def fp8_store(x: torch.Tensor, out: Fp8 | None = None) -> Fp8:
 @_on_stream
 def fp8_store_weight(w: torch.Tensor, transposed: bool = False, out: Fp8 | None = None, out_t: Fp8 | None = None):
     """w in e4m3 with a scale for each block of 128 x 128; with transposed=True (w8, wt8), wt8 being w^T
-    in the same codes: fp8_linear(x, w8) is the layer, fp8_linear(dy, wt8) its input's gradient."""
+    in the same codes: fp8_linear(x, w8) is the layer, fp8_linear(dy, wt8) its input's gradient.  out and out_t
+    are two."""
     ld = _matrix(w, "w")
     rows, cols = w.shape
     dev = w.device
@@ -729,7 +730,7 @@ def block_norm_forward(x: torch.Tensor, weight: torch.Tensor | None = None, h: t
     block_norm_backward needs.  Without `h`, x' is x (the norm alone); without `weight` there is no y;
     without `post_weight` the block's end is h as it is.  gate: float32 [cols], a matrix like x, or None
     for 1.  Weights are float32 [cols].  p, seed, offset, counter: as of dropout (which h is needed for).
-    `out` may be x or h, and `y` may be h."""
+    `out` may be x or h, and `y` may be h, but not `out`."""
     ldx = _matrix(x, "x")
     rows, cols = x.shape
     dev, dtype = x.device, x.dtype

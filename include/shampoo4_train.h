@@ -221,7 +221,7 @@ SHAMPOO4_API shampoo4_status shampoo4_fp8_store(shampoo4_dtype dtype, int64_t ro
 
 /* Quantises a weight W:[rows, cols], with block_rows = 128, and, unless t_codes and t_scales are
  * both NULL, writes W^T:[cols, rows] too (the same codes and scales, for the gradient of the
- * layer's input). */
+ * layer's input; EINVAL: into the same memory). */
 SHAMPOO4_API shampoo4_status shampoo4_fp8_store_weight(shampoo4_dtype dtype, int64_t rows, int64_t cols, const void* w,
                                                        int64_t ldw, uint8_t* codes, uint8_t* scales,
                                                        uint8_t* t_codes, uint8_t* t_scales, void* stream);
@@ -294,7 +294,7 @@ SHAMPOO4_API shampoo4_status shampoo4_dropout(const shampoo4_dropout_config* cfg
  * rstd and h_rstd, fp32 [rows], receive the two factors for the backward pass (NULL: none).
  * y_codes and y_scales (both or none) receive y as rounded, quantised as by shampoo4_fp8_store:
  * the next product's operand.  With h NULL, residual_scale must be 1, and post_weight, gate, out
- * and h_rstd NULL.  out may be x or h itself, and y may be h, each with its leading dimension.
+ * and h_rstd NULL.  out may be x or h itself, and y may be h, each with its leading dimension (EINVAL: y is out).
  * With h NULL nothing is dropped.  A gate that is not finite makes NaN where it is dropped too, in x' (0 gate) and
  * in the backward pass, where what is dropped is g.
  * eps: at least 1e-30, finite.  Finite rows of any size have their norm (squares beyond fp32 are taken
@@ -323,8 +323,8 @@ SHAMPOO4_API shampoo4_status shampoo4_block_norm_forward(const shampoo4_block_no
  *     dh = h_rstd (u - hh mean(u hh))     (post_weight NULL: z = drop(h), dh = d)
  * dx, dh and a matrix dgate are of `dtype` and may be NULL; dweight, dpost_weight and a vector dgate
  * are fp32 [cols], written in whole (rows = 0: zeros), and may be NULL.  dx may be dres or dy itself,
- * dh may be h or dy or dres (but not what dx is), each with its leading dimension.  What is not needed for the
- * outputs asked for may still be read.  The workspace (NULL when the size is 0) holds partial sums.
+ * dh may be h or dy or dres (EINVAL: what dx is, or a matrix dgate), each with its leading dimension.  What is not
+ * needed for the outputs asked for may still be read.  The workspace (NULL when the size is 0) holds partial sums.
  * Sums over rows are in fp32, of fixed groups of rows in order. */
 SHAMPOO4_API size_t shampoo4_block_norm_workspace_bytes(int64_t rows, int64_t cols);
 SHAMPOO4_API shampoo4_status shampoo4_block_norm_backward(const shampoo4_block_norm_config* cfg, shampoo4_dtype dtype,
